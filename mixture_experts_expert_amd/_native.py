@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe_native (the C ABI in include/moe_native.h).
+"""ctypes binding of libmoe_native (the C ABI in include/moe_native.h and
+include/moe_lowbit.h).
 
 Argument marshalling only: every function takes torch tensors for the
 device buffers, checks dtype/device/contiguity/size on the host, passes raw
@@ -19,6 +20,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_native.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_native.h")
+LOWBIT_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_lowbit.h")
 PROBE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_probe.h")
 
 if not os.path.exists(LIB_PATH):
@@ -79,6 +81,18 @@ _SIGNATURES = {
     "moe_grouped_fc1_wgrad_accum": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64,
                                                    _vp, _vp]),
     "moe_route_bwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _vp, _vp]),
+    "moe_w4_quantize": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    "moe_w4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
+    "moe_q8_quantize": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    "moe_q8_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
+    "moe_grouped_fc1_swiglu_w4": (ctypes.c_int, [_vp] * 8 + [_i64, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "moe_grouped_fc2_w4": (ctypes.c_int, [_vp] * 6 + [_i64, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "moe_gather_combine_f32": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _vp, _vp]),
+    "moe_grouped_ffn_w4": (ctypes.c_int, [_vp] * 11 + [_i64, _i32, _i32, _i32, _i32]
+                           + [_vp] * 4),
+    "moe_grouped_fc1_swiglu_save_q8": (ctypes.c_int, [_vp] * 4 + [_i64, _i32, _i32, _i32, _i64]
+                                       + [_vp] * 4),
+    "moe_swiglu_bwd_q8": (ctypes.c_int, [_vp] * 4 + [_i64, _i32] + [_vp] * 4),
     "moe_probe_read": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp, _vp]),
     "moe_probe_write": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp]),
     "moe_probe_copy": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp]),
@@ -626,3 +640,196 @@ def moe_route_bwd(topk_ids, topk_probs, token_routes, d_prob, d_logits, stream=N
         _ptr(token_routes, torch.int32, N * K, "token_routes"),
         _ptr(d_prob, torch.float32, R, "d_prob"), N, E, K, R,
         _ptr(d_logits, torch.float32, N * E, "d_logits"), _stream(stream)))
+
+
+# ------------------------------------------------- block-scaled storage forms
+
+def _here(stream, **tensors):
+    """All of a call's tensors (and its stream, if it names a device) must be
+    on the current device, where the kernels are launched.  Returns the stream."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    where = getattr(stream, "device", None)
+    if where is not None and torch.device(where).index not in (None, dev):
+        raise ValueError(f"the stream is on {where}, the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def _pieces(wide, name: str, per_byte: int, codes, scales):
+    """Rows and columns of a block-scaled tensor, from its bf16 form."""
+    if wide.dim() < 1 or wide.shape[-1] < 1:
+        raise ValueError(f"{name} must have at least one column")
+    cols = wide.shape[-1]
+    rows = wide.numel() // cols
+    lead = tuple(wide.shape[:-1])
+    if cols % 32 or tuple(codes.shape) != lead + (cols // per_byte,) \
+            or tuple(scales.shape) != lead + (cols // 32,):
+        raise ValueError(f"codes and scales must be [..., {cols}/{per_byte}] and [..., {cols}/32] "
+                         f"with {name} [..., {cols}]")
+    return rows, cols
+
+
+def moe_w4_quantize(w, codes, scales, stream=None):
+    """bf16 w [..., K] -> 4-bit codes uint8 [..., K/2], scales uint8 [..., K/32]."""
+    st = _here(stream, w=w, codes=codes, scales=scales)
+    rows, K = _pieces(w, "w", 2, codes, scales)
+    _check("moe_w4_quantize", lib.moe_w4_quantize(
+        _ptr(w, torch.bfloat16, rows * K, "w"), rows, K,
+        _ptr(codes, torch.uint8, rows * K // 2, "codes"),
+        _ptr(scales, torch.uint8, rows * K // 32, "scales"), st))
+
+
+def moe_w4_dequantize(codes, scales, w, stream=None):
+    """The bf16 values w [..., K] that 4-bit codes stand for (exact)."""
+    st = _here(stream, codes=codes, scales=scales, w=w)
+    rows, K = _pieces(w, "w", 2, codes, scales)
+    _check("moe_w4_dequantize", lib.moe_w4_dequantize(
+        _ptr(codes, torch.uint8, rows * K // 2, "codes"),
+        _ptr(scales, torch.uint8, rows * K // 32, "scales"), rows, K,
+        _ptr(w, torch.bfloat16, rows * K, "w"), st))
+
+
+def moe_q8_quantize(v, codes, scales, stream=None):
+    """bf16 v [..., D] -> codes int8 [..., D], scales uint8 [..., D/32]."""
+    st = _here(stream, v=v, codes=codes, scales=scales)
+    rows, D = _pieces(v, "v", 1, codes, scales)
+    _check("moe_q8_quantize", lib.moe_q8_quantize(
+        _ptr(v, torch.bfloat16, rows * D, "v"), rows, D, _ptr(codes, torch.int8, rows * D, "codes"),
+        _ptr(scales, torch.uint8, rows * D // 32, "scales"), st))
+
+
+def moe_q8_dequantize(codes, scales, v, stream=None):
+    """The bf16 values v [..., D] that 8-bit codes stand for (exact)."""
+    st = _here(stream, codes=codes, scales=scales, v=v)
+    rows, D = _pieces(v, "v", 1, codes, scales)
+    _check("moe_q8_dequantize", lib.moe_q8_dequantize(
+        _ptr(codes, torch.int8, rows * D, "codes"),
+        _ptr(scales, torch.uint8, rows * D // 32, "scales"), rows, D,
+        _ptr(v, torch.bfloat16, rows * D, "v"), st))
+
+
+def _w4_shape(codes, scales, name: str):
+    """(E, rows, columns) of 4-bit weights [E, rows, cols/2] with scales [E, rows, cols/32]."""
+    if codes.dim() != 3 or tuple(scales.shape) != (*codes.shape[:2], codes.shape[2] // 16) \
+            or codes.shape[2] % 16:
+        raise ValueError(f"{name} must be codes [E, rows, cols/2] with scales [E, rows, cols/32]")
+    return codes.shape[0], codes.shape[1], codes.shape[2] * 2
+
+
+def _w4_list(N: int, K: int, E: int, expert_ids, block_start, route_counts):
+    R = moe_dropless_bound(N, K, E)
+    return R, (_ptr(expert_ids, torch.int32, R // moe_layout_block_m(), "expert_ids"),
+               _ptr(block_start, torch.int32, E, "block_start"),
+               _ptr(route_counts, torch.int32, E, "route_counts"))
+
+
+def moe_grouped_fc1_swiglu_w4(x, w1_codes, w1_scales, sorted_slot_ids, slot_probs, expert_ids,
+                              block_start, route_counts, K: int, act, stream=None):
+    """act [R, I] = silu(gate) * up * prob of the dropless routes, on 4-bit weights
+    (codes [E, 2I, H/2], scales [E, 2I, H/32]).  Rows of pad slots are not written."""
+    st = _here(stream, x=x, w1_codes=w1_codes, w1_scales=w1_scales, sorted_slot_ids=sorted_slot_ids,
+               slot_probs=slot_probs, expert_ids=expert_ids, block_start=block_start,
+               route_counts=route_counts, act=act)
+    N, H = x.shape
+    E, I2, H1 = _w4_shape(w1_codes, w1_scales, "w1")
+    I = I2 // 2
+    if H1 != H or I2 % 2:
+        raise ValueError("w1 must be [E, 2I, H] with x [N, H]")
+    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    _check("moe_grouped_fc1_swiglu_w4", lib.moe_grouped_fc1_swiglu_w4(
+        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1_codes, torch.uint8, E * I * H, "w1_codes"),
+        _ptr(w1_scales, torch.uint8, E * I * H // 16, "w1_scales"),
+        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
+        _ptr(slot_probs, torch.float32, R, "slot_probs"), *lst, N, H, I, E, K,
+        _ptr(act, torch.bfloat16, R * I, "act"), st))
+
+
+def moe_grouped_fc2_w4(act, w2_codes, w2_scales, expert_ids, block_start, route_counts, N: int,
+                       K: int, route_out, stream=None):
+    """route_out [R, H] (float32) = act W2^T of the dropless routes, on 4-bit weights
+    (codes [E, H, I/2], scales [E, H, I/32]).  Rows of pad slots are not written."""
+    st = _here(stream, act=act, w2_codes=w2_codes, w2_scales=w2_scales, expert_ids=expert_ids,
+               block_start=block_start, route_counts=route_counts, route_out=route_out)
+    E, H, I = _w4_shape(w2_codes, w2_scales, "w2")
+    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    _check("moe_grouped_fc2_w4", lib.moe_grouped_fc2_w4(
+        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(w2_codes, torch.uint8, E * H * I // 2, "w2_codes"),
+        _ptr(w2_scales, torch.uint8, E * H * I // 32, "w2_scales"), *lst, N, H, I, E, K,
+        _ptr(route_out, torch.float32, R * H, "route_out"), st))
+
+
+def moe_gather_combine_f32(route_out, token_routes, y, stream=None):
+    """moe_gather_combine over float32 rows: y bf16 [N, H], rounded once."""
+    st = _here(stream, route_out=route_out, token_routes=token_routes, y=y)
+    N, K = token_routes.shape
+    R, H = route_out.shape
+    _check("moe_gather_combine_f32", lib.moe_gather_combine_f32(
+        _ptr(route_out, torch.float32, R * H, "route_out"),
+        _ptr(token_routes, torch.int32, N * K, "token_routes"), N, K, H, R,
+        _ptr(y, torch.bfloat16, N * H, "y"), st))
+
+
+def moe_grouped_ffn_w4(x, w1_codes, w1_scales, w2_codes, w2_scales, sorted_slot_ids, slot_probs,
+                       expert_ids, block_start, route_counts, token_routes, act, route_out, y,
+                       stream=None):
+    """Steps 4-5 of the dropless form on 4-bit weights: FC1 + SwiGLU * prob into act, FC2 into
+    route_out (float32), each token's sum into y."""
+    st = _here(stream, x=x, w1_codes=w1_codes, w1_scales=w1_scales, w2_codes=w2_codes,
+               w2_scales=w2_scales, sorted_slot_ids=sorted_slot_ids, slot_probs=slot_probs,
+               expert_ids=expert_ids, block_start=block_start, route_counts=route_counts,
+               token_routes=token_routes, act=act, route_out=route_out, y=y)
+    N, H = x.shape
+    K = token_routes.shape[1]
+    E, I2, H1 = _w4_shape(w1_codes, w1_scales, "w1")
+    I = I2 // 2
+    if H1 != H or I2 % 2 or _w4_shape(w2_codes, w2_scales, "w2") != (E, H, I):
+        raise ValueError("weights must be w1 [E, 2I, H] and w2 [E, H, I] with x [N, H]")
+    if token_routes.shape[0] != N:
+        raise ValueError("token_routes must be [N, K] with x [N, H]")
+    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    _check("moe_grouped_ffn_w4", lib.moe_grouped_ffn_w4(
+        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1_codes, torch.uint8, E * I * H, "w1_codes"),
+        _ptr(w1_scales, torch.uint8, E * I * H // 16, "w1_scales"),
+        _ptr(w2_codes, torch.uint8, E * H * I // 2, "w2_codes"),
+        _ptr(w2_scales, torch.uint8, E * H * I // 32, "w2_scales"),
+        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
+        _ptr(slot_probs, torch.float32, R, "slot_probs"), *lst,
+        _ptr(token_routes, torch.int32, N * K, "token_routes"), N, H, I, E, K,
+        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(route_out, torch.float32, R * H, "route_out"),
+        _ptr(y, torch.bfloat16, N * H, "y"), st))
+
+
+def moe_grouped_fc1_swiglu_save_q8(x, w1, sorted_slot_ids, slot_probs, C: int, act, codes, scales,
+                                   stream=None):
+    """moe_grouped_fc1_swiglu that also keeps the pre-activation in 8 bits:
+    codes int8 [R, 2I], scales uint8 [R, 2I/32]."""
+    st = _here(stream, x=x, w1=w1, sorted_slot_ids=sorted_slot_ids, slot_probs=slot_probs, act=act,
+               codes=codes, scales=scales)
+    N, H, I, E = _ffn_shape(x, w1)
+    R = E * moe_padded_capacity(C)
+    _check("moe_grouped_fc1_swiglu_save_q8", lib.moe_grouped_fc1_swiglu_save_q8(
+        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1, torch.bfloat16, E * 2 * I * H, "w1"),
+        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
+        _ptr(slot_probs, torch.float32, R, "slot_probs"), N, H, I, E, C,
+        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(codes, torch.int8, R * 2 * I, "codes"),
+        _ptr(scales, torch.uint8, R * I // 16, "scales"), st))
+
+
+def moe_swiglu_bwd_q8(codes, scales, d_act, slot_probs, act, d_preact, d_prob, stream=None):
+    """moe_swiglu_bwd with the pre-activation in 8 bits (codes [R, 2I], scales [R, 2I/32])."""
+    st = _here(stream, codes=codes, scales=scales, d_act=d_act, slot_probs=slot_probs, act=act,
+               d_preact=d_preact, d_prob=d_prob)
+    R, I = d_act.shape
+    _check("moe_swiglu_bwd_q8", lib.moe_swiglu_bwd_q8(
+        _ptr(codes, torch.int8, R * 2 * I, "codes"), _ptr(scales, torch.uint8, R * I // 16, "scales"),
+        _ptr(d_act, torch.bfloat16, R * I, "d_act"), _ptr(slot_probs, torch.float32, R, "slot_probs"),
+        R, I, _ptr(act, torch.bfloat16, R * I, "act"),
+        _ptr(d_preact, torch.bfloat16, R * 2 * I, "d_preact"),
+        _ptr(d_prob, torch.float32, R, "d_prob"), st))

@@ -41,6 +41,7 @@
 #include <initializer_list>
 
 #include "gemm_common.h"
+#include "lowbit.h"
 #include "slot_gemm.h"
 
 namespace moe {
@@ -54,7 +55,8 @@ struct FfnArgs {
     const int* sorted_slot_ids;   // FC1 only
     const float* slot_probs;      // FC1 only
     uint16_t* out;                // FC1: act [E*Cp, I]; FC2: route_out [E*Cp, H]
-    uint16_t* preact;             // FC1 only, may be null: raw [gate | up] [E*Cp, 2I]
+    void* preact;                 // FC1 only, may be null: raw [gate | up] [E*Cp, 2I], bf16 or (scales) int8 codes
+    uint8_t* scales;              // the codes' scale bytes [E*Cp, 2I/32], or null
     int N;                        // tokens (FC1 sentinel row)
     int Kdim;                     // contraction length: FC1 H, FC2 I
     int ncols;                    // output columns: FC1 I, FC2 H
@@ -83,7 +85,7 @@ struct FfnArgs {
 // a swap of lane halves leaves 8 consecutive bf16 columns per lane for one
 // 16-byte store.
 template <int BMT, int BNT, int WM, int WN, int BK, int NA, int NB, bool FC1, bool DYN,
-          bool SAVE = false, int EPI = 0>
+          int SAVE = 0, int EPI = 0>
 __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
     constexpr int NW = WM * WN;
     constexpr int WTM = BMT / WM;
@@ -100,10 +102,13 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
     constexpr int B_INST = BNT / RPI / NW;
     constexpr int LOADS = A_INST + B_INST;                 // per wave per K slab
     constexpr int OUT_COLS = FC1 ? BNT / 2 : BNT;          // output columns of a tile
-    // 16-byte stores per lane per tile (FC1 with SAVE also stores the raw
-    // gate and up columns, the pre-activation the backward keeps)
-    constexpr int STORES = FC1 ? (SAVE ? 3 : 1) * MI * NI : 2 * MI * NI;
+    // stores per lane per tile (FC1 with SAVE also stores the raw gate and up
+    // columns, the pre-activation the backward keeps: 1 as bf16, two more
+    // 16-byte stores a block; 2 as 8-bit codes, one 16-byte store of gate and
+    // of up codes and one scale byte a row block)
+    constexpr int STORES = FC1 ? (SAVE == 1 ? 3 : 1) * MI * NI + (SAVE == 2 ? 3 * MI : 0) : 2 * MI * NI;
     static_assert(FC1 || !SAVE, "only FC1 has a pre-activation");
+    static_assert(SAVE != 2 || NI == 2, "a wave's 32 gate columns are one scale group");
     constexpr int LDS_BYTES = NA * A_STAGE + NB * B_STAGE;
     // Step j issues A(j+NA-1) then B(j+NB-1); vector-memory operations retire
     // in issue order.  Before computing slab kt, the newer of A(kt) and B(kt)
@@ -496,9 +501,62 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
         const __amdgpu_buffer_rsrc_t orsrc = __builtin_amdgcn_make_buffer_rsrc(
             p.out + static_cast<int64_t>(cur.seg) * p.ncols, static_cast<short>(0),
             cur.len * p.ncols * 2, kRsrcWord3);
+        constexpr int PRE_BYTES = SAVE == 2 ? 1 : 2;        // of one pre-activation value
         const __amdgpu_buffer_rsrc_t prsrc = __builtin_amdgcn_make_buffer_rsrc(
-            SAVE ? p.preact + static_cast<int64_t>(cur.seg) * 2 * p.ncols : p.out, static_cast<short>(0),
-            SAVE ? cur.len * p.ncols * 4 : 0, kRsrcWord3);
+            SAVE ? static_cast<void*>(static_cast<uint8_t*>(p.preact) +
+                                      static_cast<int64_t>(cur.seg) * 2 * p.ncols * PRE_BYTES)
+                 : static_cast<void*>(p.out),
+            static_cast<short>(0), SAVE ? cur.len * p.ncols * 2 * PRE_BYTES : 0, kRsrcWord3);
+        const int srow = 2 * p.ncols / kGroup;              // scale bytes of a row
+        const __amdgpu_buffer_rsrc_t srsrc = __builtin_amdgcn_make_buffer_rsrc(
+            SAVE == 2 ? static_cast<void*>(p.scales + static_cast<int64_t>(cur.seg) * srow)
+                      : static_cast<void*>(p.out),
+            static_cast<short>(0), SAVE == 2 ? cur.len * srow : 0, kRsrcWord3);
+        // SAVE 2: the 8-bit codes of row block mi.  The lane pair (l, l + 32)
+        // holds the row's 32 gate and 32 up columns, one scale group each: one
+        // swap of halves leaves the gate's two maxima in the lower lane and the
+        // up's in the upper, which takes that group's scale byte; another hands
+        // both factors to both.  The codes of the lane's 16 columns, half*16 ..
+        // of the wave's 32, come out as one 16-byte piece of gate and of up.
+        // Stores the scale byte.
+        auto fc1_q8 = [&](int mi, u32x4 (&codes)[2]) {
+            uint32_t m[2] = {0, 0};
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    m[0] = max(m[0], abs_bits(acc[mi][ni][j]));
+                    m[1] = max(m[1], abs_bits(acc[mi][ni][8 + j]));
+                }
+            const auto mm = __builtin_amdgcn_permlane32_swap(m[0], m[1], false, false);
+            const int b = q8_scale_byte(max(mm[0], mm[1]));
+            const uint32_t iv = __float_as_uint(inv_scale(b));
+            const auto ii = __builtin_amdgcn_permlane32_swap(iv, iv, false, false);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const float inv = __uint_as_float(ii[part]);
+                uint32_t d[2][2];
+#pragma unroll
+                for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const floatx16& v = acc[mi][NI == 2 ? ni : 0];
+                        const int j = 8 * part + 4 * g;
+                        const uint32_t w = q8_pack4(v[j], v[j + 1], v[j + 2], v[j + 3], inv);
+                        d[ni][g] = ii[part] == 0 ? 0 : w;   // a group that stands for NaN
+                    }
+                const auto s0 = __builtin_amdgcn_permlane32_swap(d[0][0], d[1][0], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(d[0][1], d[1][1], false, false);
+                codes[part][0] = s0[0]; codes[part][1] = s0[1];
+                codes[part][2] = s1[0]; codes[part][3] = s1[1];
+            }
+            const int row = cur.m0 + wm * WTM + mi * 32 + (lane & 31);
+            const int col = cur.nt * OUT_COLS + wn * WTN / 2;   // the wave's first column: a whole group
+            __builtin_amdgcn_raw_buffer_store_b8(
+                static_cast<uint8_t>(b), srsrc,
+                row < cur.len && col < p.ncols
+                    ? static_cast<uint32_t>(row) * srow + (col + half * p.ncols) / kGroup : kOob, 0, 0);
+        };
         // FC1: the lane's 8 activations of block (mi, ni), tile columns
         // (wn*WTN + ni*32)/2 + 8*half ..
         auto fc1_act = [&](int mi, int ni) {
@@ -542,8 +600,9 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                 // chunks, swizzled by row) of a 128-column tile: rows
                 // [base, base + CAP) of the tile go there per round, then 16
                 // lanes write each row whole.  Parts: the activation, then
-                // (SAVE) the raw gate and up columns of the same rows, at col
-                // and I + col of preact.
+                // (SAVE 1) the raw gate and up columns of the same rows, at col
+                // and I + col of preact, or (SAVE 2) both as 8-bit codes, the
+                // row's 128 gate and 128 up bytes side by side.
                 constexpr int ROWS_A = A_STAGE / 256, CAP = ROWS_A + B_STAGE / 256;
                 static_assert(OUT_COLS == 128 && CAP % 32 == 0, "staged FC1 rows");
                 auto so = [&](int sr, int c) {
@@ -568,7 +627,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                 };
                 bool started = false;
 #pragma unroll
-                for (int part = 0; part < (SAVE ? 3 : 1); ++part) {
+                for (int part = 0; part < (SAVE == 1 ? 3 : SAVE == 2 ? 2 : 1); ++part) {
 #pragma unroll
                     for (int base = 0; base < BMT; base += CAP) {
                         if (started) __syncthreads();      // the previous round is read back
@@ -577,6 +636,15 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                         for (int mi = 0; mi < MI; ++mi) {
                             const int r0 = wm * WTM + mi * 32;   // the block's first tile row
                             if (r0 < base || r0 >= base + CAP) continue;
+                            if (SAVE == 2 && part == 1) {
+                                u32x4 codes[2];
+                                fc1_q8(mi, codes);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    *(lds_u32x4*)((lds_u8*)smem + so(r0 - base + (lane & 31), h * 8 + wn * 2 + half)) =
+                                        codes[h];
+                                continue;
+                            }
 #pragma unroll
                             for (int ni = 0; ni < NI; ++ni)
                                 *(lds_u32x4*)((lds_u8*)smem + so(r0 - base + (lane & 31),
@@ -595,6 +663,12 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                             if (part == 0) {
                                 __builtin_amdgcn_raw_buffer_store_b128(
                                     v, orsrc, live ? (static_cast<uint32_t>(row) * p.ncols + col) * 2u : kOob, 0, POLICY);
+                            } else if (SAVE == 2) {
+                                const int qcol = cur.nt * OUT_COLS + (c & 7) * 16;
+                                const uint32_t qoff = static_cast<uint32_t>(row) * 2u * p.ncols + qcol +
+                                                      (c >> 3) * static_cast<uint32_t>(p.ncols);
+                                __builtin_amdgcn_raw_buffer_store_b128(
+                                    v, prsrc, sr < cnt && row < cur.len && qcol < p.ncols ? qoff : kOob, 0, POLICY);
                             } else {
                                 const uint32_t poff = (static_cast<uint32_t>(row) * 2u * p.ncols + col +
                                                        (part - 1) * static_cast<uint32_t>(p.ncols)) * 2u;
@@ -653,7 +727,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                         const bool live = row < cur.len && col < p.ncols;
                         const uint32_t off = live ? (static_cast<uint32_t>(row) * p.ncols + col) * 2u : kOob;
                         __builtin_amdgcn_raw_buffer_store_b128(fc1_act(mi, ni), orsrc, off, 0, 0);
-                        if (SAVE) {
+                        if (SAVE == 1) {
                             // the same columns of the raw gate (acc[0..7]) and up
                             // (acc[8..15]) rows, at col and I + col of the row
                             const floatx16& v = acc[mi][ni];
@@ -688,6 +762,16 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                         }
                     }
                 }
+                if constexpr (SAVE == 2) {
+                    u32x4 codes[2];
+                    fc1_q8(mi, codes);
+                    const int col = cur.nt * OUT_COLS + wn * WTN / 2 + 16 * half;
+                    const uint32_t qoff = row < cur.len && col < p.ncols
+                        ? static_cast<uint32_t>(row) * 2u * p.ncols + col : kOob;
+                    __builtin_amdgcn_raw_buffer_store_b128(codes[0], prsrc, qoff, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        codes[1], prsrc, qoff == kOob ? kOob : qoff + static_cast<uint32_t>(p.ncols), 0, 0);
+                }
             }
         }
         zero_acc();
@@ -712,7 +796,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
 }
 
 template <int BMT, int BNT, int WM, int WN, int BK, int NA, int NB, bool FC1, bool DYN,
-          bool SAVE = false, int EPI = 0>
+          int SAVE = 0, int EPI = 0>
 void launch_persistent(const FfnArgs& a, hipStream_t s) {
     constexpr int threads = WM * WN * kWave;
     auto* k = ffn_gemm_kernel<BMT, BNT, WM, WN, BK, NA, NB, FC1, DYN, SAVE, EPI>;
@@ -750,12 +834,13 @@ int launch_gemm(FfnArgs a, bool fc1, int E, hipStream_t s, bool dyn = false) {
     constexpr bool STAGED = SHAPE && BMT == 256;
     constexpr bool STAGED2 = SHAPE && (BMT == 256 || BMT == 320);
     if (dyn) {
-        if (fc1) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, true, false, STAGED ? 2 : 0>(a, s);
-        else launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, false, true, false, STAGED2 ? 1 : 0>(a, s);
+        if (fc1) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, true, 0, STAGED ? 2 : 0>(a, s);
+        else launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, false, true, 0, STAGED2 ? 1 : 0>(a, s);
     } else {
-        if (fc1 && a.preact) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, false, true, STAGED ? 2 : 0>(a, s);
-        else if (fc1) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, false, false, STAGED ? 2 : 0>(a, s);
-        else launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, false, false, false, STAGED2 ? 1 : 0>(a, s);
+        if (fc1 && a.scales) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, false, 2, STAGED ? 2 : 0>(a, s);
+        else if (fc1 && a.preact) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, false, 1, STAGED ? 2 : 0>(a, s);
+        else if (fc1) launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, true, false, 0, STAGED ? 2 : 0>(a, s);
+        else launch_persistent<BMT, BNT, WM, WN, BK, NA, NB, false, false, 0, STAGED2 ? 1 : 0>(a, s);
     }
     return MOE_OK;
 }
@@ -911,6 +996,26 @@ extern "C" int moe_grouped_fc1_swiglu_save(const uint16_t* x, const uint16_t* w1
     if (st != MOE_OK) return st;
     FfnArgs a = fc1_args(x, w1, sorted_slot_ids, slot_probs, N, H, I, Cp, act);
     a.preact = preact;
+    st = launch(a, true, E, stream);
+    return st != MOE_OK ? st : launch_status();
+}
+
+extern "C" int moe_grouped_fc1_swiglu_save_q8(const uint16_t* x, const uint16_t* w1,
+                                              const int32_t* sorted_slot_ids, const float* slot_probs,
+                                              int64_t N, int32_t H, int32_t I, int32_t E, int64_t C,
+                                              uint16_t* act, int8_t* codes, uint8_t* scales,
+                                              hipStream_t stream) {
+    using namespace moe;
+    int Cp = 0;
+    int st = check_ffn(N, H, I, E, C, &Cp);
+    if (st != MOE_OK) return st;
+    if (static_cast<int64_t>(Cp) * I * 4 >= (static_cast<int64_t>(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (N == 0 || C == 0) return MOE_OK;
+    st = check_ptrs({x, w1, sorted_slot_ids, slot_probs, act, codes, scales});
+    if (st != MOE_OK) return st;
+    FfnArgs a = fc1_args(x, w1, sorted_slot_ids, slot_probs, N, H, I, Cp, act);
+    a.preact = codes;
+    a.scales = scales;
     st = launch(a, true, E, stream);
     return st != MOE_OK ? st : launch_status();
 }

@@ -11,6 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import _native as nat
+from .lowbit import is_w4
 
 
 class MoEBuffers:
@@ -92,10 +93,18 @@ class MoEBackwardBuffers:
     gradients main_dw1 / main_dw2 (gradient accumulation over micro-batches;
     zeroed here, never reset by backward) instead of being written as bf16
     dw1 / dw2.
+
+    checkpoint="q8": the pre-activation, the step's one large tensor that
+    lives from the forward to the backward, is kept as 8-bit codes with a
+    scale byte per 32 columns (preact_codes, preact_scales: 52% of the bf16
+    bytes) instead of bf16 preact.
     """
 
-    def __init__(self, fwd: MoEBuffers, main_grad: bool = False):
+    def __init__(self, fwd: MoEBuffers, main_grad: bool = False, checkpoint: str = "bf16"):
+        if checkpoint not in ("bf16", "q8"):
+            raise ValueError('checkpoint must be "bf16" or "q8"')
         self.f = fwd
+        self.checkpoint = checkpoint
         R, N, H, I, E = fwd.R, fwd.N, fwd.H, fwd.I, fwd.E
         dev = fwd.act.device
         bf16, f32 = torch.bfloat16, torch.float32
@@ -103,7 +112,11 @@ class MoEBackwardBuffers:
         def z(shape, dt):
             return torch.zeros(shape, dtype=dt, device=dev)
 
-        self.preact = z((R, 2 * I), bf16)
+        if checkpoint == "q8":
+            self.preact_codes = z((R, 2 * I), torch.int8)
+            self.preact_scales = z((R, 2 * I // 32), torch.uint8)
+        else:
+            self.preact = z((R, 2 * I), bf16)
         self.d_act = z((R, I), bf16)
         self.act_re = z((R, I), bf16)
         self.d_preact = z((R, 2 * I), bf16)
@@ -121,6 +134,10 @@ class MoEBackwardBuffers:
 
     def fc1_swiglu_save(self, x, w1, stream=None):
         f = self.f
+        if self.checkpoint == "q8":
+            nat.moe_grouped_fc1_swiglu_save_q8(x, w1, f.sorted_slot_ids, f.slot_probs, f.C, f.act,
+                                               self.preact_codes, self.preact_scales, stream)
+            return
         nat.moe_grouped_fc1_swiglu_save(x, w1, f.sorted_slot_ids, f.slot_probs, f.C, f.act,
                                         self.preact, stream)
 
@@ -137,6 +154,10 @@ class MoEBackwardBuffers:
         nat.moe_grouped_fc2_dgrad(dy, w2, self.f.sorted_slot_ids, self.f.C, self.d_act, stream)
 
     def swiglu_bwd(self, stream=None):
+        if self.checkpoint == "q8":
+            nat.moe_swiglu_bwd_q8(self.preact_codes, self.preact_scales, self.d_act,
+                                  self.f.slot_probs, self.act_re, self.d_preact, self.d_prob, stream)
+            return
         nat.moe_swiglu_bwd(self.preact, self.d_act, self.f.slot_probs, self.act_re,
                            self.d_preact, self.d_prob, stream)
 
@@ -190,9 +211,12 @@ def forward(buf: MoEBuffers, logits, x, w1, w2, stream=None):
 class DroplessBuffers:
     """Device buffers for the dropless variant: every route kept, expert
     segments padded to whole blocks, the route list sized to its static bound
-    Rd = moe_dropless_bound(N, K, E) and the real extent a device scalar."""
+    Rd = moe_dropless_bound(N, K, E) and the real extent a device scalar.
 
-    def __init__(self, N: int, H: int, I: int, E: int, K: int, device="cuda"):
+    w4=True: for 4-bit weights (W4Weights); route_out is float32."""
+
+    def __init__(self, N: int, H: int, I: int, E: int, K: int, device="cuda", w4: bool = False):
+        self.w4 = bool(w4)
         self.N, self.H, self.I, self.E, self.K = N, H, I, E, K
         self.BM = nat.moe_layout_block_m()
         self.R = nat.moe_dropless_bound(N, K, E)
@@ -214,7 +238,7 @@ class DroplessBuffers:
         self.token_route_count = z((N,), i32)
         self.num_tokens_post_padded = z((1,), i32)
         self.act = z((self.R, I), bf16)
-        self.route_out = z((self.R, H), bf16)
+        self.route_out = z((self.R, H), f32 if self.w4 else bf16)
         self.y = z((N, H), bf16)
         self.workspace = nat.route_workspace(N, E, K, dev)   # the routing map
 
@@ -240,12 +264,29 @@ class DroplessBuffers:
                                      self.N, self.K, self.route_out, stream)
 
     def combine(self, stream=None):
-        nat.moe_gather_combine(self.route_out, self.token_routes, self.y, stream)
+        if self.w4:
+            nat.moe_gather_combine_f32(self.route_out, self.token_routes, self.y, stream)
+        else:
+            nat.moe_gather_combine(self.route_out, self.token_routes, self.y, stream)
+
+    def ffn_w4(self, x, w1, w2, stream=None):
+        """FC1, FC2 and the combine on 4-bit weights (buffers built with w4=True)."""
+        nat.moe_grouped_ffn_w4(x, w1.codes, w1.scales, w2.codes, w2.scales, self.sorted_slot_ids,
+                               self.slot_probs, self.expert_ids, self.block_start,
+                               self.route_counts, self.token_routes, self.act, self.route_out,
+                               self.y, stream)
 
 
 def forward_dropless(buf: DroplessBuffers, logits, x, w1, w2, stream=None):
-    """The dropless variant on one stream; returns buf.y (bf16 [N, H])."""
+    """The dropless variant on one stream; returns buf.y (bf16 [N, H]).  Weights
+    in bf16, or both W4Weights with buffers built with w4=True."""
+    w4 = is_w4(w1, w2)
+    if w4 != buf.w4:
+        raise ValueError("4-bit weights need DroplessBuffers(..., w4=True), bf16 weights w4=False")
     buf.route(logits, stream)
+    if w4:
+        buf.ffn_w4(x, w1, w2, stream)
+        return buf.y
     buf.grouped_ffn(x, w1, w2, stream)
     buf.combine(stream)
     return buf.y

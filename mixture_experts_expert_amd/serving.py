@@ -30,6 +30,7 @@ import math
 import torch
 
 from . import _native as nat
+from .lowbit import is_w4
 
 # Bucket sizes as multiples of the expected item size: dense just above 0.5x
 # and 1.0x, then coarser up to the ceiling.
@@ -74,11 +75,13 @@ class BucketLadder:
 
 class ServingLadder:
     """Dropless MoE FFN forward for items of 1..max_tokens tokens, replayed
-    from per-bucket graphs that share one set of static buffers."""
+    from per-bucket graphs that share one set of static buffers.  w1 and w2
+    are bf16 tensors, or both W4Weights (4-bit expert weights)."""
 
     def __init__(self, w1, w2, K: int, expected: int, max_tokens: int, device="cuda",
                  max_padding_ratio: float = 1.25, reserve_bytes: int = 8 << 30,
                  factors=DEFAULT_FACTORS, mem_get_info=None):
+        self.w4 = is_w4(w1, w2)
         self.E, I2, self.H = w1.shape
         self.I = I2 // 2
         self.K = K
@@ -95,7 +98,7 @@ class ServingLadder:
         self.x = torch.zeros((N, H), dtype=torch.bfloat16, device=dev)
         self.n_live = torch.zeros((1,), dtype=torch.int32, device=dev)
         from .forward import DroplessBuffers
-        self.buf = DroplessBuffers(N, H, self.I, E, K, dev)
+        self.buf = DroplessBuffers(N, H, self.I, E, K, dev, w4=self.w4)
         self.graphs = {}
         self.stream = torch.cuda.Stream(device=dev)
         self.counts = {"eager": 0}
@@ -115,6 +118,12 @@ class ServingLadder:
                                    b.route_counts, b.sorted_slot_ids, b.slot_probs, b.expert_ids,
                                    b.block_start, b.token_routes[:n], b.token_route_count[:n],
                                    b.num_tokens_post_padded, b.workspace)
+        if self.w4:
+            nat.moe_grouped_ffn_w4(self.x[:n], self.w1.codes, self.w1.scales, self.w2.codes,
+                                   self.w2.scales, b.sorted_slot_ids, b.slot_probs, b.expert_ids,
+                                   b.block_start, b.route_counts, b.token_routes[:n], b.act,
+                                   b.route_out, b.y[:n])
+            return
         nat.moe_grouped_ffn_fwd_dropless(self.x[:n], self.w1, self.w2, b.sorted_slot_ids,
                                          b.slot_probs, b.block_start, b.num_tokens_post_padded,
                                          K, b.act, b.route_out)

@@ -17,7 +17,8 @@ Pages followed (cited by title and section):
   gather-combine.
 
 Parity status per function is listed in the module docstrings of
-``oracle.moe`` (forward) and ``oracle.backward`` (backward).
+``oracle.moe`` (forward), ``oracle.backward`` (backward) and
+``oracle.lowbit`` (block-scaled storage).
 """
 
 from .moe import (  # noqa: F401
@@ -57,4 +58,14 @@ from .backward import (  # noqa: F401
     main_grad_accumulate,
     route_backward,
     swiglu_backward,
+)
+from .lowbit import (  # noqa: F401
+    q8_quantize,
+    q8_values,
+    scale_of,
+    w4_ffn_rows,
+    w4_pack,
+    w4_quantize,
+    w4_unpack,
+    w4_values,
 )
