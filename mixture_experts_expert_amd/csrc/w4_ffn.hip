@@ -6,24 +6,31 @@
 //   y[t]         = bf16( sum_k route_out[token_routes[t, k]] )
 //
 // With a handful of rows per expert the weights' bytes are the time: every
-// byte of an expert in use is read once, for all of its rows, and everything
-// else is kept out of the way of that stream.
-//   * A lane's 16-byte load of codes is one group of 32 columns, so it takes
-//     one scale byte, and the codes go from memory to registers without LDS.
-//     gfx950's v_cvt_scalef32_pk_bf16_fp4 turns two codes into two scaled bf16
-//     (exact: a 2-bit significand times a power of two) in one instruction:
+// byte of an expert in use is read once for up to 32 of its rows, and
+// everything else is kept out of the way of that stream.
+//   * gfx950's v_cvt_scalef32_pk_bf16_fp4 turns two codes into two scaled bf16
+//     (exact: a 2-bit significand times a power of two) in one instruction,
 //     half a vector instruction per weight.
-//   * The products are 16x16x32 bf16 MFMAs with the weight rows as the first
+//   * The products are 16x16x32 bf16 MFMAs with 16 weight rows as the first
 //     operand and up to 16 routes as the second.  A contraction may run over
-//     its columns in any order that both operands share: lane group q takes
-//     columns 32q .. 32q+31 of a 128-wide step, which four MFMAs consume 8 at
-//     a time, so both operands load straight from their rows.
-//   * The workgroup's four waves split the contraction in 128-wide steps and
-//     add their sums in wave order through LDS.  The split depends on the
-//     contraction's length alone, so a route's result is the same, bit for
-//     bit, whatever else is in the batch.
-//   * FC1 pairs gate and up rows in one workgroup, so the SwiGLU and the
-//     route's probability are applied to the sums in registers.
+//     its columns in any order that both operands share: a 16-byte piece of
+//     codes is one scale group of a row, and a lane's two pieces of a 256-wide
+//     step feed eight MFMAs as they come.
+//   * A row's scale bytes are loaded for 2048 columns at once and kept in LDS.
+//     Loaded step by step, 8 bytes of each of 64 rows, they took a quarter of
+//     the time (a wide layer's FC1 266 us against 186 without them, 174 now).
+//   * A contraction is summed in four parts, added in order.  With few tiles
+//     (w4_split_kernel) the four waves of a workgroup take a part each; with
+//     many (w4_stream_kernel) every wave runs all four for its own rows and
+//     the routes' rows are shared through LDS.  The additions are the same, so
+//     a route's result is the same, bit for bit, whatever else is in the batch.
+//   * FC1 pairs gate and up rows in one wave, so the SwiGLU and the route's
+//     probability are applied to the sums in registers.
+//   * The weights' first loads leave as soon as the expert is known, before
+//     the block's row count and tokens are.
+//
+// One token of a layer of 128 experts (8 a token, H 2048, I 768): FC1 6.1 us,
+// FC2 3.7 us; 16 tokens 33 + 16 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights.
 #include <algorithm>
 #include <initializer_list>
 
@@ -34,10 +41,14 @@ namespace moe {
 namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kW4Waves = 4;      // waves of a workgroup; they split the contraction
-constexpr int kW4Step = 128;     // columns of a step: four lane groups of one scale group each
+constexpr int kW4Step = 256;     // columns of a step: 128 bytes of codes a row, 8 scale bytes
+constexpr int kW4Parts = 4;      // parts of a contraction, summed apart and added in order
+constexpr int kW4Waves = 4;      // waves of a workgroup of the grouped kernel
+constexpr int kW4Panel = 8;      // steps whose scale bytes are staged together
+constexpr int kW4Pitch = 72;     // LDS bytes of a weight row's panel: 64, and 8 that spread the banks
 
 struct W4Args {
     const uint16_t* a;           // FC1: x [N, H]; FC2: act [R, I]
@@ -57,7 +68,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint3
                                              static_cast<int>(bytes), kRsrcWord3);
 }
 
-// 8 codes (one word) as 8 bf16 times 2^(exponent of scale).
+// 8 codes (one word) as 8 bf16 times 2^(b - 127), the scale byte b in the
+// float's exponent field: the instruction reads that field alone, so b = 0
+// is 2^-127 and b = 255 makes every value NaN.
 __device__ __forceinline__ bf16x8 w4_values(uint32_t word, float scale) {
     const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 0);
     const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, scale, 1);
@@ -69,152 +82,452 @@ __device__ __forceinline__ bf16x8 w4_values(uint32_t word, float scale) {
     return r;
 }
 
-// One workgroup: output columns 16*RT * blockIdx.x .. of the routes
-// [rel*BM, rel*BM + 16*CT) of one expert, rel the layout block's place in the
-// expert's segment.  WT weight tiles of 16 rows: FC1 has a gate and an up
-// tile for each of its RT column tiles.
-template <bool FC1, int RT, int CT>
-__global__ __launch_bounds__(kW4Waves * kWave) void w4_gemm_kernel(W4Args p) {
-    constexpr int WT = FC1 ? 2 * RT : RT;
-    constexpr int U = CT == 1 ? 4 : 2;                  // steps whose loads are in flight together
-    static_assert(CT <= 2 || CT % 2 == 0, "whole layout blocks");
-    __shared__ floatx4 s_acc[kW4Waves][WT * CT][kWave];
-
-    // the layout block's expert and rows: device data, range-checked
-    const int b = blockIdx.y;
-    const int e = p.expert_ids[b];
-    if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) return;      // past the extent
-    const int rel = b - p.block_start[e];
-    if (rel < 0 || rel % ((16 * CT + kBlockM - 1) / kBlockM) != 0) return;   // another workgroup's rows
-    const int slot0 = b * kBlockM;
-    const int n = min(min(p.route_counts[e] - rel * kBlockM, 16 * CT), p.R - slot0);
-    if (n <= 0) return;
-
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-    const int r16 = lane & 15, q = lane >> 4;
-    const int col0 = blockIdx.x * (16 * RT);            // first output column
-
-    // per-lane byte offsets of the weight rows (out-of-range rows read zeros)
-    const int64_t base = static_cast<int64_t>(e) * p.wrows;
-    const __amdgpu_buffer_rsrc_t crs = buffer(p.codes + base * (p.Kdim / 2), static_cast<uint32_t>(p.wrows) * (p.Kdim / 2));
-    const __amdgpu_buffer_rsrc_t srs = buffer(p.scales + base * (p.Kdim / kGroup), static_cast<uint32_t>(p.wrows) * (p.Kdim / kGroup));
-    uint32_t coff[WT], soff[WT];
+// One 256-wide step of one 16-row weight tile against CT column tiles.  Lane
+// (r16, q) holds the codes of columns 64q .. 64q+63 of its row, 8 a word; any
+// order of the contraction will do that both operands share, so the i-th MFMA
+// takes every lane group's i-th word, and the other operand's lanes columns
+// 64q + 8i .. +7 of their rows.  sc: the lane's two scale bytes.
+template <int CT>
+__device__ __forceinline__ void w4_step(const u32x4 (&cw)[2], uint32_t sc, const u32x4 (&xw)[CT][8], floatx4 (&acc)[CT]) {
 #pragma unroll
-    for (int t = 0; t < WT; ++t) {
-        const int col = col0 + (FC1 ? t / 2 : t) * 16 + r16;
-        const int row = FC1 && (t & 1) ? p.ncols + col : col;
-        coff[t] = col < p.ncols ? static_cast<uint32_t>(row) * (p.Kdim / 2) + q * 16 : kOob;
-        soff[t] = col < p.ncols ? static_cast<uint32_t>(row) * (p.Kdim / kGroup) + q : kOob;
+    for (int i = 0; i < 8; ++i) {
+        const float scale = __uint_as_float((sc >> (8 * (i >> 2)) & 255u) << 23);
+        const bf16x8 a = w4_values(cw[i >> 2][i & 3], scale);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, xw[c][i]), acc[c], 0, 0, 0);
     }
-    // and of the routes' rows
-    const __amdgpu_buffer_rsrc_t ars = FC1
-        ? buffer(p.a, static_cast<uint32_t>(p.N) * p.Kdim * 2u)
-        : buffer(p.a + static_cast<int64_t>(slot0) * p.Kdim, static_cast<uint32_t>(n) * p.Kdim * 2u);
-    uint32_t aoff[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int i = c * 16 + r16;
-        int row = i < n ? i : -1;
-        if (FC1 && i < n) row = p.sorted_slot_ids[slot0 + i];
-        const int rows = FC1 ? p.N : n;
-        aoff[c] = static_cast<unsigned>(row) < static_cast<unsigned>(rows)
-            ? static_cast<uint32_t>(row) * p.Kdim * 2u + q * 64 : kOob;
+}
+
+// First step of part i of a contraction of `steps` steps.
+__device__ __forceinline__ int w4_part(int steps, int i) { return steps * i / kW4Parts; }
+
+// What a wave knows of its weights: WT tiles of 16 rows (FC1: a gate and an up
+// tile for each of its WT/2 output column tiles) from output column col0 on.
+// SALIGN: rows of scale bytes are whole words (Kdim a multiple of 128).
+template <bool FC1, int WT, bool SALIGN>
+struct W4Rows {
+    static constexpr int ROWS = 16 * WT;
+    static constexpr int RT = FC1 ? WT / 2 : WT;        // output column tiles
+    static constexpr int SREGS = SALIGN ? kW4Panel * 2 : kW4Panel * 2 + 1;
+    static_assert(ROWS <= kWave, "a row of scales a lane");
+    const W4Args& p;
+    const int lane, wave, r16, q, steps, sbytes;
+    int lo, hi;                  // the wave's steps
+    int col0, slot0, n;          // first output column and slot, live routes
+    __amdgpu_buffer_rsrc_t codes, scales, rows;
+    uint32_t soff, shift;
+    uint32_t sv[SREGS];
+    uint8_t* s_scale;            // the wave's LDS panel of scale bytes
+
+    __device__ __forceinline__ W4Rows(const W4Args& a, bool split)
+        : p(a), lane(threadIdx.x & (kWave - 1)),
+          wave(__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave)),
+          r16(lane & 15), q(lane >> 4), steps((a.Kdim + kW4Step - 1) / kW4Step), sbytes(a.Kdim / kGroup) {
+        lo = split ? w4_part(steps, wave) : 0;
+        hi = split ? w4_part(steps, wave + 1) : steps;
     }
 
-    floatx4 acc[WT][CT];
-#pragma unroll
-    for (int t = 0; t < WT; ++t)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) acc[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ int row_of(int t, int r) const {   // weight row r of tile t, or -1
+        const int col = col0 + (FC1 ? t / 2 : t) * 16 + r;
+        return col < p.ncols ? (FC1 && (t & 1) ? p.ncols + col : col) : -1;
+    }
+    __device__ __forceinline__ uint32_t code_offset(int t, int r, int byte) const {
+        const int row = row_of(t, r);
+        return row >= 0 ? static_cast<uint32_t>(row) * (p.Kdim / 2) + byte : kOob;
+    }
 
-    // this wave's steps
-    const int steps = (p.Kdim + kW4Step - 1) / kW4Step;
-    const int lo = steps * wave / kW4Waves, hi = steps * (wave + 1) / kW4Waves;
-    for (int k0 = lo; k0 < hi; k0 += U) {
-        u32x4 cw[U][WT], xw[U][CT][4];
-        uint32_t sb[U][WT];
+    // Descriptors of expert e's weights; rows past the last read zeros.
+    __device__ __forceinline__ void weights(int e) {
+        const int64_t base = static_cast<int64_t>(e) * p.wrows;
+        codes = buffer(p.codes + base * (p.Kdim / 2), static_cast<uint32_t>(p.wrows) * (p.Kdim / 2));
+        scales = buffer(p.scales + base * sbytes, static_cast<uint32_t>(p.wrows) * sbytes);
+        const int row = lane < ROWS ? row_of(lane >> 4, lane & 15) : -1;
+        soff = row >= 0 ? static_cast<uint32_t>(row) * sbytes : kOob;
+        shift = (soff & 2) * 8;
+        soff &= ~3u;
+    }
+    // The block's live routes, and the descriptor of their rows.  False: none.
+    __device__ __forceinline__ bool routes(int b, int e) {
+        const int rel = b - p.block_start[e];
+        n = rel < 0 ? 0 : min(min(p.route_counts[e] - rel * kBlockM, kBlockM), p.R - slot0);
+        if (n <= 0) return false;
+        rows = FC1 ? buffer(p.a, static_cast<uint32_t>(p.N) * p.Kdim * 2u)
+                   : buffer(p.a + static_cast<int64_t>(slot0) * p.Kdim, static_cast<uint32_t>(n) * p.Kdim * 2u);
+        return true;
+    }
+    // Byte offset of column byte `byte` of route i's row, which FC1 finds at
+    // token `tok`; a route that is none reads zeros.
+    __device__ __forceinline__ uint32_t row_offset(int i, int tok, int byte) const {
+        const int row = FC1 ? tok : i;
+        return i < n && static_cast<unsigned>(row) < static_cast<unsigned>(FC1 ? p.N : n)
+            ? static_cast<uint32_t>(row) * p.Kdim * 2u + byte : kOob;
+    }
+
+    // The scale bytes of the panel that starts at step kp, one weight row a
+    // lane, in words.  Where rows are not whole words, every other row starts in
+    // the middle of one: then one word more is loaded, and the pieces are put
+    // together on the way to LDS.  Bytes past the row's end (the next row's,
+    // which may stand for NaN) become 0.
+    __device__ __forceinline__ int panel_bytes(int kp) const {
+        return min(min(kW4Panel, hi - kp) * 8, sbytes - kp * 8);
+    }
+    __device__ __forceinline__ void load_scales(int kp) {
+        const int cnt = panel_bytes(kp);
+        const uint32_t at = soff + kp * 8;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u;
-            // a lane group past the row's end, or a step past the wave's, reads zeros
-            const bool live = k < hi && k * kW4Step + q * 32 < p.Kdim;
+        for (int i = 0; i < SREGS; ++i) sv[i] = 0;
+        if (SALIGN) {
 #pragma unroll
-            for (int t = 0; t < WT; ++t) {
-                cw[u][t] = __builtin_amdgcn_raw_buffer_load_b128(crs, live ? coff[t] + k * (kW4Step / 2) : kOob, 0, kStoreNT);
-                sb[u][t] = __builtin_amdgcn_raw_buffer_load_b8(srs, live ? soff[t] + k * (kW4Step / kGroup) : kOob, 0, 0);
-            }
+            for (int i = 0; i < kW4Panel * 2; i += 4) {
+                if (i * 4 + 16 <= cnt) {
+                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(scales, at + i * 4, 0, 0);
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+                    for (int j = 0; j < 4; ++j) sv[i + j] = v[j];
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    xw[u][c][j] = __builtin_amdgcn_raw_buffer_load_b128(ars, live ? aoff[c] + k * (kW4Step * 2) + j * 16 : kOob, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int t = 0; t < WT; ++t) {
-                const float scale = __uint_as_float(sb[u][t] << 23);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 w = w4_values(cw[u][t][j], scale);
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-                        acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            w, __builtin_bit_cast(bf16x8, xw[u][c][j]), acc[t][c], 0, 0, 0);
+                    for (int j = i; j < i + 4; ++j)
+                        if (j * 4 < cnt) sv[j] = __builtin_amdgcn_raw_buffer_load_b32(scales, at + j * 4, 0, 0);
                 }
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < SREGS; ++i)
+                if (i * 4 < cnt + 2) sv[i] = __builtin_amdgcn_raw_buffer_load_b32(scales, at + i * 4, 0, 0);
+        }
+    }
+    // The panel is the wave's own: its LDS operations are in order, the fences
+    // keep the compiler from moving reads and writes past each other.
+    __device__ __forceinline__ void store_scales(int kp) {
+        const int cnt = panel_bytes(kp);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < kW4Panel; ++i) {
+            u32x2 v;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int w = 2 * i + h;
+                v[h] = SALIGN ? sv[w] : __builtin_amdgcn_alignbit(sv[SALIGN ? w : w + 1], sv[w], shift);
+                if (!SALIGN) v[h] = w * 4 >= cnt ? 0u : w * 4 + 2 == cnt ? v[h] & 0xFFFFu : v[h];
+            }
+            if (lane < ROWS) *reinterpret_cast<u32x2*>(s_scale + lane * kW4Pitch + i * 8) = v;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // The lane's two scale bytes of tile t, at step k of a panel that starts at kp.
+    __device__ __forceinline__ uint32_t scale_pair(int t, int k, int kp) const {
+        return *reinterpret_cast<const uint16_t*>(s_scale + (t * 16 + r16) * kW4Pitch + (k - kp) * 8 + q * 2);
     }
 
-    // the waves' sums, added in wave order
-#pragma unroll
-    for (int t = 0; t < WT; ++t)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) s_acc[wave][t * CT + c][lane] = acc[t][c];
-    __syncthreads();
-    auto sum = [&](int t, int c) {
-        floatx4 v = s_acc[0][t * CT + c][lane];
-#pragma unroll
-        for (int w = 1; w < kW4Waves; ++w) v += s_acc[w][t * CT + c][lane];
-        return v;
-    };
-    // lane: route c*16 + r16, output columns col0 + 16t + 4q .. +3
-    for (int i = wave; i < RT * CT; i += kW4Waves) {
-        const int t = i / CT, c = i % CT;
-        const int route = c * 16 + r16, col = col0 + 16 * t + 4 * q;
-        if (route >= n || col >= p.ncols) continue;
+    // Output tile t of one route: the lane's 4 columns col0 + 16t + 4q .. +3,
+    // from the sums sum(weight tile).
+    template <class SUM>
+    __device__ __forceinline__ void put(int t, int route, SUM sum) const {
+        const int col = col0 + 16 * t + 4 * q;
+        if (route >= n || col >= p.ncols) return;
         const int64_t at = static_cast<int64_t>(slot0 + route) * p.ncols + col;
         if (FC1) {
-            const floatx4 g = sum(2 * t, c), u = sum(2 * t + 1, c);
+            const floatx4 g = sum(2 * t), u = sum(2 * t + 1);
             const float pr = p.slot_probs[slot0 + route];
             uint2 o;
             o.x = pack_bf16x2(silu(g[0]) * u[0] * pr, silu(g[1]) * u[1] * pr);
             o.y = pack_bf16x2(silu(g[2]) * u[2] * pr, silu(g[3]) * u[3] * pr);
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = o;
         } else {
-            *reinterpret_cast<floatx4*>(static_cast<float*>(p.out) + at) = sum(t, c);
+            *reinterpret_cast<floatx4*>(static_cast<float*>(p.out) + at) = sum(t);
         }
+    }
+};
+
+// ---------------------------------------------------------------- few tiles
+// Workgroup (x, y): WT weight tiles and layout block y; wave w sums part w of
+// the contraction.  Every load goes straight to operand registers, the
+// shortest way when a wave has one step or two.  Lane (r16, q) takes the 32
+// bytes of codes of columns 64q .. 64q+63 of its row, and the other operand's
+// lanes those columns of their rows.
+template <bool FC1, int WT, bool SALIGN>
+struct W4Split : W4Rows<FC1, WT, SALIGN> {
+    typedef W4Rows<FC1, WT, SALIGN> B;
+    using B::p; using B::lane; using B::wave; using B::r16; using B::q; using B::lo; using B::hi; using B::n;
+    uint32_t coff[WT];
+    u32x4 cw[WT][2];
+
+    __device__ __forceinline__ explicit W4Split(const W4Args& a) : B(a, true) {}
+
+    __device__ __forceinline__ void load_codes(int k) {
+        const bool live = k * kW4Step + q * 64 < p.Kdim;   // past the row's end: zeros
+#pragma unroll
+        for (int t = 0; t < WT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                cw[t][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                    this->codes, live ? coff[t] + k * (kW4Step / 2) + h * 16 : kOob, 0, 0);
+    }
+
+    // Routes c0 .. c0 + 16*CT - 1.  fetched: the first step's codes and scales
+    // are already on their way.
+    template <int CT>
+    __device__ __forceinline__ void run(int c0, const int* tok, bool fetched, floatx4* s_acc) {
+        uint32_t aoff[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) aoff[c] = this->row_offset(c0 + c * 16 + r16, tok[c], q * 128);
+        floatx4 acc[WT][CT];
+#pragma unroll
+        for (int t = 0; t < WT; ++t)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = lo, kp = lo; k < hi; ++k) {
+            if (k - kp == kW4Panel) kp = k;
+            if (!(fetched && k == lo)) {
+                if (k == kp) this->load_scales(k);
+                load_codes(k);
+            }
+            u32x4 xw[CT][8];
+            const bool live = k * kW4Step + q * 64 < p.Kdim;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    xw[c][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                        this->rows, live ? aoff[c] + k * (kW4Step * 2) + i * 16 : kOob, 0, 0);
+            // every load of the step is issued before the first result is waited for
+            __builtin_amdgcn_sched_barrier(0);
+            if (k == kp) this->store_scales(k);
+#pragma unroll
+            for (int t = 0; t < WT; ++t) w4_step<CT>(cw[t], this->scale_pair(t, k, kp), xw, acc[t]);
+        }
+        // the parts meet in LDS, in the place of the scale panels
+        __syncthreads();
+        floatx4* mine = s_acc + wave * WT * CT * kWave + lane;
+#pragma unroll
+        for (int t = 0; t < WT; ++t)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) mine[(t * CT + c) * kWave] = acc[t][c];
+        __syncthreads();
+        for (int i = wave; i < B::RT * CT; i += kW4Waves) {
+            const int c = i % CT;
+            this->put(i / CT, c0 + 16 * c + r16, [&](int t) {
+                const floatx4* at = s_acc + (t * CT + c) * kWave + lane;
+                floatx4 v = at[0];
+#pragma unroll
+                for (int j = 1; j < kW4Parts; ++j) v += at[j * WT * CT * kWave];
+                return v;
+            });
+        }
+    }
+};
+
+// CTMAX: the most 16-route tiles held at once; with 1, a block of more than 16
+// routes reads its weights twice, the second time from the caches.
+template <bool FC1, int WT, int CTMAX, bool SALIGN>
+__global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
+    typedef W4Split<FC1, WT, SALIGN> Wave;
+    constexpr int SCALE_BYTES = kW4Waves * Wave::ROWS * kW4Pitch;
+    constexpr int ACC_BYTES = kW4Waves * WT * CTMAX * kWave * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[SCALE_BYTES > ACC_BYTES ? SCALE_BYTES : ACC_BYTES];
+    static_assert(kW4Waves == kW4Parts, "a part a wave");
+    Wave w(p);
+    const int b = blockIdx.y;                           // < R / BM
+    w.slot0 = b * kBlockM;
+    int tok[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) tok[c] = FC1 ? p.sorted_slot_ids[w.slot0 + c * 16 + w.r16] : 0;
+    const int e = p.expert_ids[b];                      // device data: range-checked
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) return;      // past the extent
+    w.s_scale = smem + w.wave * (Wave::ROWS * kW4Pitch);
+    w.col0 = blockIdx.x * (16 * Wave::RT);
+    w.weights(e);
+#pragma unroll
+    for (int t = 0; t < WT; ++t) w.coff[t] = w.code_offset(t, w.r16, w.q * 32);
+    if (w.lo < w.hi) {
+        w.load_scales(w.lo);
+        w.load_codes(w.lo);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (!w.routes(b, e)) return;
+    floatx4* const s_acc = reinterpret_cast<floatx4*>(smem);
+    if (CTMAX == 1) {
+        w.template run<1>(0, tok, true, s_acc);
+        if (w.n > 16) {
+            __syncthreads();                            // the sums are read
+            w.template run<1>(16, tok + 1, false, s_acc);
+        }
+    } else if (w.n <= 16) {
+        w.template run<1>(0, tok, true, s_acc);
+    } else {
+        w.template run<CTMAX>(0, tok, true, s_acc);
+    }
+}
+
+// --------------------------------------------------------------- many tiles
+// Workgroup (x, y): the weight tiles of its four waves, WT each, and layout
+// block y.  Loads straight to operand registers take 64 cache accesses each,
+// since neighbouring lanes are different rows; that, not memory, bounded them
+// (the address units 60% busy).  Here codes come in whole lines, 8 rows of 128
+// bytes a load, and the routes' rows once for the four waves; both pass
+// through LDS into operand layout (16-byte pieces, swizzled by row: no bank
+// conflicts), and the next step's loads run beside this step's products.
+// 128 tokens of the 128-expert layer: FC1 44 us (52 straight to registers),
+// FC2 27 us (32).
+template <bool FC1, int WT, bool SALIGN>
+struct W4Stream : W4Rows<FC1, WT, SALIGN> {
+    typedef W4Rows<FC1, WT, SALIGN> B;
+    using B::p; using B::lane; using B::wave; using B::r16; using B::q; using B::steps; using B::n;
+    uint32_t coff[2 * WT];
+    u32x4 cr[2 * WT];            // codes on their way
+    uint8_t* s_codes;            // the wave's own
+    uint8_t* s_rows;             // the workgroup's
+
+    __device__ __forceinline__ explicit W4Stream(const W4Args& a) : B(a, false) {}
+
+    __device__ __forceinline__ void load_codes(int k) {
+        const bool live = k * kW4Step + lane % 8 * 32 < p.Kdim;   // past the row's end: zeros
+#pragma unroll
+        for (int i = 0; i < 2 * WT; ++i)
+            cr[i] = __builtin_amdgcn_raw_buffer_load_b128(this->codes, live ? coff[i] + k * (kW4Step / 2) : kOob, 0, 0);
+    }
+
+    template <int CT>
+    __device__ __forceinline__ void run(int c0, bool fetched) {
+        // the wave brings 4 rows of each 16-row tile, two a load, 512 bytes each
+        uint32_t aoff[CT][2];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = c0 + c * 16 + 4 * wave + 2 * j + lane / 32;
+                aoff[c][j] = this->row_offset(i, FC1 && i < n ? p.sorted_slot_ids[this->slot0 + i] : -1, lane % 32 * 16);
+            }
+        u32x4 xr[CT][2];
+        auto load_rows = [&](int k) {
+            const bool live = k * kW4Step + lane % 32 * 8 < p.Kdim;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    xr[c][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                        this->rows, live ? aoff[c][j] + k * (kW4Step * 2) : kOob, 0, 0);
+        };
+        floatx4 acc[WT][CT], tot[WT][CT];
+#pragma unroll
+        for (int t = 0; t < WT; ++t)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[t][c] = tot[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!fetched) {
+            this->load_scales(0);
+            load_codes(0);
+        }
+        load_rows(0);
+        for (int k = 0, kp = 0, part = 0; k < steps; ++k) {
+            if (k - kp == kW4Panel) kp = k;
+            __builtin_amdgcn_sched_barrier(0);
+            if (k > 0) __syncthreads();                 // the last step's rows are read
+            if (k == kp) this->store_scales(k);
+#pragma unroll
+            for (int i = 0; i < 2 * WT; ++i) {
+                const int row = 8 * i + lane / 8;
+                *reinterpret_cast<u32x4*>(s_codes + row * 128 + ((lane % 8) ^ (row / 2 % 8)) * 16) = cr[i];
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = 4 * wave + 2 * j + lane / 32;
+                    *reinterpret_cast<u32x4*>(s_rows + c * 8192 + row * 512 + ((lane % 32) ^ row) * 16) = xr[c][j];
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            if (k + 1 < steps) {
+                if (k + 1 - kp == kW4Panel) this->load_scales(k + 1);
+                load_codes(k + 1);
+                load_rows(k + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();                            // the rows are there
+            u32x4 xw[CT][8];
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    xw[c][i] = *reinterpret_cast<const u32x4*>(s_rows + c * 8192 + r16 * 512 + ((q * 8 + i) ^ r16) * 16);
+            // past a part's last step: its sums join the total
+            while (part < kW4Parts - 1 && k >= w4_part(steps, part + 1)) {
+                ++part;
+#pragma unroll
+                for (int t = 0; t < WT; ++t)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        tot[t][c] += acc[t][c];
+                        acc[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < WT; ++t) {
+                u32x4 cw[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    cw[h] = *reinterpret_cast<const u32x4*>(s_codes + (t * 16 + r16) * 128 + ((q * 2 + h) ^ (r16 / 2 % 8)) * 16);
+                w4_step<CT>(cw, this->scale_pair(t, k, kp), xw, acc[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < B::RT; ++t)
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                this->put(t, c0 + 16 * c + r16, [&](int i) { return tot[i][c] + acc[i][c]; });
+    }
+};
+
+template <bool FC1, int WT, int CTMAX, bool SALIGN>
+__global__ __launch_bounds__(kW4Waves * kWave) void w4_stream_kernel(W4Args p) {
+    typedef W4Stream<FC1, WT, SALIGN> Wave;
+    constexpr int SCALE = Wave::ROWS * kW4Pitch, CODES = Wave::ROWS * 128, ROWS = CTMAX * 8192;
+    __shared__ __attribute__((aligned(256))) uint8_t smem[ROWS + kW4Waves * (CODES + SCALE)];
+    Wave w(p);
+    const int b = blockIdx.y;                           // < R / BM
+    w.slot0 = b * kBlockM;
+    const int e = p.expert_ids[b];                      // device data: range-checked
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) return;      // past the extent
+    w.s_rows = smem;
+    w.s_codes = smem + ROWS + w.wave * CODES;
+    w.s_scale = smem + ROWS + kW4Waves * CODES + w.wave * SCALE;
+    w.col0 = (blockIdx.x * kW4Waves + w.wave) * (16 * Wave::RT);
+    w.weights(e);
+#pragma unroll
+    for (int i = 0; i < 2 * WT; ++i) w.coff[i] = w.code_offset(i / 2, i % 2 * 8 + w.lane / 8, w.lane % 8 * 16);
+    w.load_scales(0);
+    w.load_codes(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!w.routes(b, e)) return;                        // uniform over the workgroup
+    if (CTMAX == 1) {
+        w.template run<1>(0, true);
+        if (w.n > 16) {
+            __syncthreads();                            // the last step's rows are read
+            w.template run<1>(16, false);
+        }
+    } else if (w.n <= 16) {
+        w.template run<1>(0, true);
+    } else {
+        w.template run<CTMAX>(0, true);
     }
 }
 
 // y[t] = bf16( sum over k, from +0.0 in k order, of the token's routes ).
-// One thread: 4 columns of one token.
+// Workgroup (x, y): 1024 columns of token y, 4 a thread; the token's routes are
+// uniform, so all K rows are on their way after one scalar load.
 template <int KMAX>
 __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restrict__ route_out,
-                                                          const int* __restrict__ token_routes, int N, int K,
-                                                          int H, int R, uint16_t* __restrict__ y) {
-    const int chunks = H / 4;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (item >= static_cast<int64_t>(N) * chunks) return;
-    const int t = static_cast<int>(item / chunks);
-    const int c = static_cast<int>(item - static_cast<int64_t>(t) * chunks);
+                                                          const int* __restrict__ token_routes, int K, int H,
+                                                          int R, uint16_t* __restrict__ y) {
+    const int64_t t = blockIdx.y;
+    const int col = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (col >= H) return;
     floatx4 v[KMAX];
 #pragma unroll
     for (int k = 0; k < KMAX; ++k) {
-        const int r = k < K ? token_routes[static_cast<int64_t>(t) * K + k] : -1;
+        const int r = k < K ? token_routes[t * K + k] : -1;
         v[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (r >= 0 && r < R)   // device data is range-checked, never trusted
-            v[k] = *reinterpret_cast<const floatx4*>(route_out + static_cast<int64_t>(r) * H + c * 4);
+        if (static_cast<unsigned>(r) < static_cast<unsigned>(R))   // device data is range-checked, never trusted
+            v[k] = *reinterpret_cast<const floatx4*>(route_out + static_cast<int64_t>(r) * H + col);
     }
     floatx4 s = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -222,13 +535,12 @@ __global__ __launch_bounds__(256) void combine_f32_kernel(const float* __restric
     uint2 o;
     o.x = pack_bf16x2(s[0], s[1]);
     o.y = pack_bf16x2(s[2], s[3]);
-    *reinterpret_cast<uint2*>(y + static_cast<int64_t>(t) * H + c * 4) = o;
+    *reinterpret_cast<uint2*>(y + t * H + col) = o;
 }
 
 template <int KMAX>
 void launch_combine_f32(const float* ro, const int* tr, int N, int K, int H, int R, uint16_t* y, hipStream_t s) {
-    const int64_t items = static_cast<int64_t>(N) * (H / 4);
-    combine_f32_kernel<KMAX><<<static_cast<unsigned>((items + 255) / 256), 256, 0, s>>>(ro, tr, N, K, H, R, y);
+    combine_f32_kernel<KMAX><<<dim3((H + 1023) / 1024, N), 256, 0, s>>>(ro, tr, K, H, R, y);
 }
 
 // Layout blocks that can hold routes: at most one partly filled block per
@@ -259,12 +571,39 @@ int check_ptrs(std::initializer_list<const void*> ptrs) {
     return MOE_OK;
 }
 
+template <bool FC1, int CTMAX>
+void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
+    constexpr int threads = kW4Waves * kWave;
+    const bool salign = a.Kdim % 128 == 0;
+    auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
+    if (tiles >= 2000) {
+        const dim3 g = grid((FC1 ? 16 : 32) * kW4Waves);
+        if (salign) w4_stream_kernel<FC1, 2, CTMAX, true><<<g, threads, 0, s>>>(a);
+        else w4_stream_kernel<FC1, 2, CTMAX, false><<<g, threads, 0, s>>>(a);
+    } else if (tiles >= 500) {
+        const dim3 g = grid(FC1 ? 32 : 64);
+        if (salign) w4_split_kernel<FC1, 4, CTMAX, true><<<g, threads, 0, s>>>(a);
+        else w4_split_kernel<FC1, 4, CTMAX, false><<<g, threads, 0, s>>>(a);
+    } else {
+        const dim3 g = grid(FC1 ? 16 : 32);
+        if (salign) w4_split_kernel<FC1, 2, CTMAX, true><<<g, threads, 0, s>>>(a);
+        else w4_split_kernel<FC1, 2, CTMAX, false><<<g, threads, 0, s>>>(a);
+    }
+}
+
+// Which kernel: by the most tiles of 64 weight rows that the route list can
+// ask for.  Under 500 (two workgroups a compute unit) the split kernel takes
+// 32-row workgroups, for more of them (3 tokens of a small layer: 8.6 us
+// against 10.0); from 2000 on the streaming one fills the device (128 tokens,
+// 128 experts: 76 us against 83 split; 4 tokens, 768 tiles: 25 us split, 27
+// streaming).  Two 16-route tiles are held at once where experts have more
+// than 10 routes on average (12 a head: 87 us against 92; 8: 80 against 76,
+// the registers of the second tile cost a workgroup a compute unit).
 template <bool FC1>
-void launch_w4(W4Args& a, int blocks, double mean, hipStream_t s) {
-    constexpr int RT = FC1 ? 2 : 4;
-    const dim3 grid((a.ncols + 16 * RT - 1) / (16 * RT), blocks);
-    if (mean > 32) w4_gemm_kernel<FC1, RT, 4><<<grid, kW4Waves * kWave, 0, s>>>(a);
-    else w4_gemm_kernel<FC1, RT, 2><<<grid, kW4Waves * kWave, 0, s>>>(a);
+void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
+    const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64));
+    if (mean > 10) launch_w4<FC1, 2>(a, blocks, tiles, s);
+    else launch_w4<FC1, 1>(a, blocks, tiles, s);
 }
 
 int ffn_w4(int which, const uint16_t* x, const uint8_t* w1_codes, const uint8_t* w1_scales,
@@ -289,12 +628,12 @@ int ffn_w4(int which, const uint16_t* x, const uint8_t* w1_codes, const uint8_t*
     if (which & 1) {
         a.a = x; a.codes = w1_codes; a.scales = w1_scales; a.sorted_slot_ids = ssi; a.slot_probs = probs;
         a.out = act; a.Kdim = H; a.ncols = I; a.wrows = 2 * I;
-        launch_w4<true>(a, blocks, mean, stream);
+        dispatch_w4<true>(a, blocks, mean, stream);
     }
     if (which & 2) {
         a.a = act; a.codes = w2_codes; a.scales = w2_scales;
         a.out = route_out; a.Kdim = I; a.ncols = H; a.wrows = H;
-        launch_w4<false>(a, blocks, mean, stream);
+        dispatch_w4<false>(a, blocks, mean, stream);
     }
     if (which & 4) return moe_gather_combine_f32(route_out, token_routes, N, K, H, R, y, stream);
     return launch_status();

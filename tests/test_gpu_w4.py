@@ -116,6 +116,13 @@ SHAPES = {
     "three_blocks_an_expert": (90, 128, 192, 3, 3),
     "many_rows": (300, 192, 128, 4, 2),
     "all_to_few": (64, 64, 64, 1000, 32),
+    # enough tiles for the streaming kernel: few and many rows an expert, steps
+    # that end inside the row, more than one panel of scales
+    "stream_few_rows": (70, 512, 1280, 64, 4),
+    "stream_many_rows": (260, 320, 704, 64, 8),
+    "stream_odd_scales": (60, 1088, 1344, 48, 8),
+    "stream_long": (40, 4160, 1536, 48, 4),
+    "split_long": (3, 4160, 2112, 4, 2),
 }
 
 
@@ -165,7 +172,7 @@ def test_three_calls_equal_the_one():
     assert torch.equal(y, y2)
 
 
-@pytest.mark.parametrize("H,I,E,K", [(1088, 448, 8, 3), (256, 2048, 4, 4)])
+@pytest.mark.parametrize("H,I,E,K", [(1088, 448, 8, 3), (256, 2048, 4, 4), (1088, 832, 48, 8), (2304, 1280, 64, 2)])
 def test_a_token_alone_equals_the_token_in_any_batch(H, I, E, K):
     N = 260                                   # up to 260 rows an expert
     buf, x, w1, w2 = case(N, H, I, E, K)
