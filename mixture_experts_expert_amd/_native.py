@@ -12,6 +12,7 @@ built, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -643,137 +644,167 @@ def moe_route_bwd(topk_ids, topk_probs, token_routes, d_prob, d_logits, stream=N
 
 
 # ------------------------------------------------- block-scaled storage forms
+#
+# These calls take a few microseconds on the device, so their arguments are
+# checked in one pass: dtype, device, contiguity and size, then the address.
 
-def _here(stream, **tensors):
-    """All of a call's tensors (and its stream, if it names a device) must be
-    on the current device, where the kernels are launched.  Returns the stream."""
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
+_BM = int(lib.moe_layout_block_m())
+_bound = functools.lru_cache(maxsize=4096)(moe_dropless_bound)
+_capacity = functools.lru_cache(maxsize=4096)(moe_padded_capacity)
+
+
+def _here(stream):
+    """The current device and the stream's handle on it.  Kernels are launched
+    on the current device: a stream of another one is refused."""
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    where = getattr(stream, "device", None)
-    if where is not None and torch.device(where).index not in (None, dev):
-        raise ValueError(f"the stream is on {where}, the current device is cuda:{dev}")
-    return _stream(stream)
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    where = getattr(stream, "device_index", None)
+    if where is not None and where != dev:
+        raise ValueError(f"the stream is on device {where}, the current device is {dev}")
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _here_of(t, name: str, stream):
+    """_here, after a look at one tensor: a host tensor is refused without
+    touching a device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return _here(stream)
+
+
+def _at(t, dtype, numel: int, name: str, dev: int) -> int:
+    """Address of a contiguous tensor of `dtype` on device `dev` with at least
+    `numel` elements; anything else is refused."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name}: needs at least {numel} elements, has {t.numel()}")
 
 
 def _pieces(wide, name: str, per_byte: int, codes, scales):
     """Rows and columns of a block-scaled tensor, from its bf16 form."""
-    if wide.dim() < 1 or wide.shape[-1] < 1:
+    for t, what in ((wide, name), (codes, "codes"), (scales, "scales")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+    v, a, b = list(wide.shape), list(codes.shape), list(scales.shape)
+    if not v or v[-1] < 1:
         raise ValueError(f"{name} must have at least one column")
-    cols = wide.shape[-1]
-    rows = wide.numel() // cols
-    lead = tuple(wide.shape[:-1])
-    if cols % 32 or tuple(codes.shape) != lead + (cols // per_byte,) \
-            or tuple(scales.shape) != lead + (cols // 32,):
-        raise ValueError(f"codes and scales must be [..., {cols}/{per_byte}] and [..., {cols}/32] "
-                         f"with {name} [..., {cols}]")
-    return rows, cols
+    cols = v.pop()
+    if cols % 32 or not a or not b or a.pop() * per_byte != cols or b.pop() * 32 != cols or a != v or b != v:
+        raise ValueError(f"codes and scales must be [..., cols/{per_byte}] and [..., cols/32] with "
+                         f"{name} [..., cols]: got {tuple(codes.shape)}, {tuple(scales.shape)} and "
+                         f"{tuple(wide.shape)}")
+    return wide.numel() // cols, cols
 
 
 def moe_w4_quantize(w, codes, scales, stream=None):
     """bf16 w [..., K] -> 4-bit codes uint8 [..., K/2], scales uint8 [..., K/32]."""
-    st = _here(stream, w=w, codes=codes, scales=scales)
     rows, K = _pieces(w, "w", 2, codes, scales)
+    dev, st = _here_of(w, "w", stream)
     _check("moe_w4_quantize", lib.moe_w4_quantize(
-        _ptr(w, torch.bfloat16, rows * K, "w"), rows, K,
-        _ptr(codes, torch.uint8, rows * K // 2, "codes"),
-        _ptr(scales, torch.uint8, rows * K // 32, "scales"), st))
+        _at(w, torch.bfloat16, 0, "w", dev), rows, K, _at(codes, torch.uint8, 0, "codes", dev),
+        _at(scales, torch.uint8, 0, "scales", dev), st))
 
 
 def moe_w4_dequantize(codes, scales, w, stream=None):
     """The bf16 values w [..., K] that 4-bit codes stand for (exact)."""
-    st = _here(stream, codes=codes, scales=scales, w=w)
     rows, K = _pieces(w, "w", 2, codes, scales)
+    dev, st = _here_of(w, "w", stream)
     _check("moe_w4_dequantize", lib.moe_w4_dequantize(
-        _ptr(codes, torch.uint8, rows * K // 2, "codes"),
-        _ptr(scales, torch.uint8, rows * K // 32, "scales"), rows, K,
-        _ptr(w, torch.bfloat16, rows * K, "w"), st))
+        _at(codes, torch.uint8, 0, "codes", dev), _at(scales, torch.uint8, 0, "scales", dev), rows,
+        K, _at(w, torch.bfloat16, 0, "w", dev), st))
 
 
 def moe_q8_quantize(v, codes, scales, stream=None):
     """bf16 v [..., D] -> codes int8 [..., D], scales uint8 [..., D/32]."""
-    st = _here(stream, v=v, codes=codes, scales=scales)
     rows, D = _pieces(v, "v", 1, codes, scales)
+    dev, st = _here_of(v, "v", stream)
     _check("moe_q8_quantize", lib.moe_q8_quantize(
-        _ptr(v, torch.bfloat16, rows * D, "v"), rows, D, _ptr(codes, torch.int8, rows * D, "codes"),
-        _ptr(scales, torch.uint8, rows * D // 32, "scales"), st))
+        _at(v, torch.bfloat16, 0, "v", dev), rows, D, _at(codes, torch.int8, 0, "codes", dev),
+        _at(scales, torch.uint8, 0, "scales", dev), st))
 
 
 def moe_q8_dequantize(codes, scales, v, stream=None):
     """The bf16 values v [..., D] that 8-bit codes stand for (exact)."""
-    st = _here(stream, codes=codes, scales=scales, v=v)
     rows, D = _pieces(v, "v", 1, codes, scales)
+    dev, st = _here_of(v, "v", stream)
     _check("moe_q8_dequantize", lib.moe_q8_dequantize(
-        _ptr(codes, torch.int8, rows * D, "codes"),
-        _ptr(scales, torch.uint8, rows * D // 32, "scales"), rows, D,
-        _ptr(v, torch.bfloat16, rows * D, "v"), st))
+        _at(codes, torch.int8, 0, "codes", dev), _at(scales, torch.uint8, 0, "scales", dev), rows,
+        D, _at(v, torch.bfloat16, 0, "v", dev), st))
 
 
 def _w4_shape(codes, scales, name: str):
     """(E, rows, columns) of 4-bit weights [E, rows, cols/2] with scales [E, rows, cols/32]."""
-    if codes.dim() != 3 or tuple(scales.shape) != (*codes.shape[:2], codes.shape[2] // 16) \
-            or codes.shape[2] % 16:
+    a, b = codes.shape, scales.shape
+    if len(a) != 3 or len(b) != 3 or a[0] != b[0] or a[1] != b[1] or a[2] != 16 * b[2]:
         raise ValueError(f"{name} must be codes [E, rows, cols/2] with scales [E, rows, cols/32]")
-    return codes.shape[0], codes.shape[1], codes.shape[2] * 2
-
-
-def _w4_list(N: int, K: int, E: int, expert_ids, block_start, route_counts):
-    R = moe_dropless_bound(N, K, E)
-    return R, (_ptr(expert_ids, torch.int32, R // moe_layout_block_m(), "expert_ids"),
-               _ptr(block_start, torch.int32, E, "block_start"),
-               _ptr(route_counts, torch.int32, E, "route_counts"))
+    return a[0], a[1], a[2] * 2
 
 
 def moe_grouped_fc1_swiglu_w4(x, w1_codes, w1_scales, sorted_slot_ids, slot_probs, expert_ids,
                               block_start, route_counts, K: int, act, stream=None):
     """act [R, I] = silu(gate) * up * prob of the dropless routes, on 4-bit weights
     (codes [E, 2I, H/2], scales [E, 2I, H/32]).  Rows of pad slots are not written."""
-    st = _here(stream, x=x, w1_codes=w1_codes, w1_scales=w1_scales, sorted_slot_ids=sorted_slot_ids,
-               slot_probs=slot_probs, expert_ids=expert_ids, block_start=block_start,
-               route_counts=route_counts, act=act)
+    dev, st = _here_of(x, "x", stream)
     N, H = x.shape
     E, I2, H1 = _w4_shape(w1_codes, w1_scales, "w1")
     I = I2 // 2
     if H1 != H or I2 % 2:
         raise ValueError("w1 must be [E, 2I, H] with x [N, H]")
-    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    R = _bound(N, K, E)
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
     _check("moe_grouped_fc1_swiglu_w4", lib.moe_grouped_fc1_swiglu_w4(
-        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1_codes, torch.uint8, E * I * H, "w1_codes"),
-        _ptr(w1_scales, torch.uint8, E * I * H // 16, "w1_scales"),
-        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
-        _ptr(slot_probs, torch.float32, R, "slot_probs"), *lst, N, H, I, E, K,
-        _ptr(act, torch.bfloat16, R * I, "act"), st))
+        _at(x, bf16, 0, "x", dev), _at(w1_codes, u8, 0, "w1_codes", dev),
+        _at(w1_scales, u8, 0, "w1_scales", dev),
+        _at(sorted_slot_ids, i32, R, "sorted_slot_ids", dev),
+        _at(slot_probs, f32, R, "slot_probs", dev),
+        _at(expert_ids, i32, R // _BM, "expert_ids", dev),
+        _at(block_start, i32, E, "block_start", dev),
+        _at(route_counts, i32, E, "route_counts", dev), N, H, I, E, K,
+        _at(act, bf16, R * I, "act", dev), st))
 
 
 def moe_grouped_fc2_w4(act, w2_codes, w2_scales, expert_ids, block_start, route_counts, N: int,
                        K: int, route_out, stream=None):
     """route_out [R, H] (float32) = act W2^T of the dropless routes, on 4-bit weights
     (codes [E, H, I/2], scales [E, H, I/32]).  Rows of pad slots are not written."""
-    st = _here(stream, act=act, w2_codes=w2_codes, w2_scales=w2_scales, expert_ids=expert_ids,
-               block_start=block_start, route_counts=route_counts, route_out=route_out)
+    dev, st = _here_of(act, "act", stream)
     E, H, I = _w4_shape(w2_codes, w2_scales, "w2")
-    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    R = _bound(N, K, E)
+    i32, u8 = torch.int32, torch.uint8
     _check("moe_grouped_fc2_w4", lib.moe_grouped_fc2_w4(
-        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(w2_codes, torch.uint8, E * H * I // 2, "w2_codes"),
-        _ptr(w2_scales, torch.uint8, E * H * I // 32, "w2_scales"), *lst, N, H, I, E, K,
-        _ptr(route_out, torch.float32, R * H, "route_out"), st))
+        _at(act, torch.bfloat16, R * I, "act", dev), _at(w2_codes, u8, 0, "w2_codes", dev),
+        _at(w2_scales, u8, 0, "w2_scales", dev),
+        _at(expert_ids, i32, R // _BM, "expert_ids", dev),
+        _at(block_start, i32, E, "block_start", dev),
+        _at(route_counts, i32, E, "route_counts", dev), N, H, I, E, K,
+        _at(route_out, torch.float32, R * H, "route_out", dev), st))
 
 
 def moe_gather_combine_f32(route_out, token_routes, y, stream=None):
     """moe_gather_combine over float32 rows: y bf16 [N, H], rounded once."""
-    st = _here(stream, route_out=route_out, token_routes=token_routes, y=y)
+    dev, st = _here_of(route_out, "route_out", stream)
     N, K = token_routes.shape
     R, H = route_out.shape
     _check("moe_gather_combine_f32", lib.moe_gather_combine_f32(
-        _ptr(route_out, torch.float32, R * H, "route_out"),
-        _ptr(token_routes, torch.int32, N * K, "token_routes"), N, K, H, R,
-        _ptr(y, torch.bfloat16, N * H, "y"), st))
+        _at(route_out, torch.float32, 0, "route_out", dev),
+        _at(token_routes, torch.int32, 0, "token_routes", dev), N, K, H, R,
+        _at(y, torch.bfloat16, N * H, "y", dev), st))
 
 
 def moe_grouped_ffn_w4(x, w1_codes, w1_scales, w2_codes, w2_scales, sorted_slot_ids, slot_probs,
@@ -781,55 +812,54 @@ def moe_grouped_ffn_w4(x, w1_codes, w1_scales, w2_codes, w2_scales, sorted_slot_
                        stream=None):
     """Steps 4-5 of the dropless form on 4-bit weights: FC1 + SwiGLU * prob into act, FC2 into
     route_out (float32), each token's sum into y."""
-    st = _here(stream, x=x, w1_codes=w1_codes, w1_scales=w1_scales, w2_codes=w2_codes,
-               w2_scales=w2_scales, sorted_slot_ids=sorted_slot_ids, slot_probs=slot_probs,
-               expert_ids=expert_ids, block_start=block_start, route_counts=route_counts,
-               token_routes=token_routes, act=act, route_out=route_out, y=y)
+    dev, st = _here_of(x, "x", stream)
     N, H = x.shape
-    K = token_routes.shape[1]
+    n, K = token_routes.shape
     E, I2, H1 = _w4_shape(w1_codes, w1_scales, "w1")
     I = I2 // 2
     if H1 != H or I2 % 2 or _w4_shape(w2_codes, w2_scales, "w2") != (E, H, I):
         raise ValueError("weights must be w1 [E, 2I, H] and w2 [E, H, I] with x [N, H]")
-    if token_routes.shape[0] != N:
+    if n != N:
         raise ValueError("token_routes must be [N, K] with x [N, H]")
-    R, lst = _w4_list(N, K, E, expert_ids, block_start, route_counts)
+    R = _bound(N, K, E)
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
     _check("moe_grouped_ffn_w4", lib.moe_grouped_ffn_w4(
-        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1_codes, torch.uint8, E * I * H, "w1_codes"),
-        _ptr(w1_scales, torch.uint8, E * I * H // 16, "w1_scales"),
-        _ptr(w2_codes, torch.uint8, E * H * I // 2, "w2_codes"),
-        _ptr(w2_scales, torch.uint8, E * H * I // 32, "w2_scales"),
-        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
-        _ptr(slot_probs, torch.float32, R, "slot_probs"), *lst,
-        _ptr(token_routes, torch.int32, N * K, "token_routes"), N, H, I, E, K,
-        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(route_out, torch.float32, R * H, "route_out"),
-        _ptr(y, torch.bfloat16, N * H, "y"), st))
+        _at(x, bf16, 0, "x", dev), _at(w1_codes, u8, 0, "w1_codes", dev),
+        _at(w1_scales, u8, 0, "w1_scales", dev), _at(w2_codes, u8, 0, "w2_codes", dev),
+        _at(w2_scales, u8, 0, "w2_scales", dev),
+        _at(sorted_slot_ids, i32, R, "sorted_slot_ids", dev),
+        _at(slot_probs, f32, R, "slot_probs", dev),
+        _at(expert_ids, i32, R // _BM, "expert_ids", dev),
+        _at(block_start, i32, E, "block_start", dev),
+        _at(route_counts, i32, E, "route_counts", dev),
+        _at(token_routes, i32, 0, "token_routes", dev), N, H, I, E, K,
+        _at(act, bf16, R * I, "act", dev), _at(route_out, f32, R * H, "route_out", dev),
+        _at(y, bf16, N * H, "y", dev), st))
 
 
 def moe_grouped_fc1_swiglu_save_q8(x, w1, sorted_slot_ids, slot_probs, C: int, act, codes, scales,
                                    stream=None):
     """moe_grouped_fc1_swiglu that also keeps the pre-activation in 8 bits:
     codes int8 [R, 2I], scales uint8 [R, 2I/32]."""
-    st = _here(stream, x=x, w1=w1, sorted_slot_ids=sorted_slot_ids, slot_probs=slot_probs, act=act,
-               codes=codes, scales=scales)
+    dev, st = _here_of(x, "x", stream)
     N, H, I, E = _ffn_shape(x, w1)
-    R = E * moe_padded_capacity(C)
+    R = E * _capacity(C)
+    bf16, u8 = torch.bfloat16, torch.uint8
     _check("moe_grouped_fc1_swiglu_save_q8", lib.moe_grouped_fc1_swiglu_save_q8(
-        _ptr(x, torch.bfloat16, N * H, "x"), _ptr(w1, torch.bfloat16, E * 2 * I * H, "w1"),
-        _ptr(sorted_slot_ids, torch.int32, R, "sorted_slot_ids"),
-        _ptr(slot_probs, torch.float32, R, "slot_probs"), N, H, I, E, C,
-        _ptr(act, torch.bfloat16, R * I, "act"), _ptr(codes, torch.int8, R * 2 * I, "codes"),
-        _ptr(scales, torch.uint8, R * I // 16, "scales"), st))
+        _at(x, bf16, 0, "x", dev), _at(w1, bf16, 0, "w1", dev),
+        _at(sorted_slot_ids, torch.int32, R, "sorted_slot_ids", dev),
+        _at(slot_probs, torch.float32, R, "slot_probs", dev), N, H, I, E, C,
+        _at(act, bf16, R * I, "act", dev), _at(codes, torch.int8, R * 2 * I, "codes", dev),
+        _at(scales, u8, R * I // 16, "scales", dev), st))
 
 
 def moe_swiglu_bwd_q8(codes, scales, d_act, slot_probs, act, d_preact, d_prob, stream=None):
     """moe_swiglu_bwd with the pre-activation in 8 bits (codes [R, 2I], scales [R, 2I/32])."""
-    st = _here(stream, codes=codes, scales=scales, d_act=d_act, slot_probs=slot_probs, act=act,
-               d_preact=d_preact, d_prob=d_prob)
+    dev, st = _here_of(d_act, "d_act", stream)
     R, I = d_act.shape
+    bf16, f32 = torch.bfloat16, torch.float32
     _check("moe_swiglu_bwd_q8", lib.moe_swiglu_bwd_q8(
-        _ptr(codes, torch.int8, R * 2 * I, "codes"), _ptr(scales, torch.uint8, R * I // 16, "scales"),
-        _ptr(d_act, torch.bfloat16, R * I, "d_act"), _ptr(slot_probs, torch.float32, R, "slot_probs"),
-        R, I, _ptr(act, torch.bfloat16, R * I, "act"),
-        _ptr(d_preact, torch.bfloat16, R * 2 * I, "d_preact"),
-        _ptr(d_prob, torch.float32, R, "d_prob"), st))
+        _at(codes, torch.int8, R * 2 * I, "codes", dev),
+        _at(scales, torch.uint8, R * I // 16, "scales", dev), _at(d_act, bf16, 0, "d_act", dev),
+        _at(slot_probs, f32, R, "slot_probs", dev), R, I, _at(act, bf16, R * I, "act", dev),
+        _at(d_preact, bf16, R * 2 * I, "d_preact", dev), _at(d_prob, f32, R, "d_prob", dev), st))

@@ -4,6 +4,7 @@
 // All are HBM-bound passes: every input is read once and every output written
 // once, 8 columns a lane (16 bytes of bf16), so a group of 32 columns is four
 // neighbouring lanes, which share its largest magnitude in two lane swaps.
+#include <algorithm>
 #include <initializer_list>
 
 #include "lowbit.h"
@@ -95,32 +96,46 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint8_t* __res
     reinterpret_cast<u16x8*>(w)[i] = o;
 }
 
-// One wave per slot row, lanes striding the I columns 8 at a time, with
-// g, u = the pre-activation's values, sig = sigmoid(g):
+// With g, u = the pre-activation's values, sig = sigmoid(g):
 //   act    = silu(g) * u * p
 //   d_gate = d_act * p * u * sig * (1 + g * (1 - sig))
 //   d_up   = d_act * p * silu(g)
-//   d_prob = sum over the row of d_act * silu(g) * u     (wave reduction)
-__global__ __launch_bounds__(256) void swiglu_bwd_q8_kernel(const int8_t* __restrict__ codes,
-                                                            const uint8_t* __restrict__ scales,
-                                                            const uint16_t* __restrict__ d_act,
-                                                            const float* __restrict__ probs, int R, int I,
-                                                            uint16_t* __restrict__ act,
-                                                            uint16_t* __restrict__ d_pre,
-                                                            float* __restrict__ d_prob) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t s = static_cast<int64_t>(blockIdx.x) * (blockDim.x / kWave) + threadIdx.x / kWave;
-    if (s >= R) return;
-    const float p = probs[s];
-    const int8_t* row = codes + s * 2 * I;
-    const uint8_t* srow = scales + s * (2 * I / kGroup);
-    float dp = 0.0f;
-    for (int c = lane * 8; c < I; c += kWave * 8) {
+//   d_prob = sum over the row of d_act * silu(g) * u
+// A workgroup takes the rows, one at least, whose 8-column pieces its threads
+// hold at once: lanes have work whatever I is (with a wave a row, I = 64 used
+// one lane in eight: 60000 rows 29 us, 8.8 now), and a thread's loads are all on
+// their way together (32768 rows of 768: 47.5 us, 5.3 TB/s; 53.3 a wave a row,
+// 48.6 with two pieces a thread).  A row is a multiple of 8 pieces: 8
+// neighbouring lanes hold 64 columns of one row, their sum goes to LDS, and 8
+// lanes add a row's sums.  The stores are of the default policy: non-temporal
+// they take this kernel to 42.6 us, but the GEMMs that read d_preact and act
+// next then find them in memory instead of the caches, and the backward as a
+// whole takes 829 us against 820.
+constexpr int kBwdThreads = 256;
+
+__global__ __launch_bounds__(kBwdThreads) void swiglu_bwd_q8_kernel(const int8_t* __restrict__ codes,
+                                                                    const uint8_t* __restrict__ scales,
+                                                                    const uint16_t* __restrict__ d_act,
+                                                                    const float* __restrict__ probs, int R, int I,
+                                                                    int per, uint16_t* __restrict__ act,
+                                                                    uint16_t* __restrict__ d_pre,
+                                                                    float* __restrict__ d_prob) {
+    __shared__ float s_dp[kMaxDim / 64];                 // of `per` rows: 256 pieces, or one row's
+    const int pieces = I / 8;                            // of a row
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(per), R - row0));
+    for (int i = threadIdx.x; i < rows * pieces; i += kBwdThreads) {
+        const int r = i / pieces, c = (i - r * pieces) * 8;
+        const int64_t s = row0 + r;
+        const int8_t* row = codes + s * 2 * I;
+        const uint8_t* srow = scales + s * (2 * I / kGroup);
         const u32x2 cg = *reinterpret_cast<const u32x2*>(row + c);
         const u32x2 cu = *reinterpret_cast<const u32x2*>(row + I + c);
         const float fg = scale_value(srow[c / kGroup]), fu = scale_value(srow[(I + c) / kGroup]);
         const u16x8 d8 = *reinterpret_cast<const u16x8*>(d_act + s * I + c);
+        const float p = probs[s];
         u16x8 a8, dg8, du8;
+        float dp = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float g = q8_float(cg[j >> 2], j & 3) * fg, u = q8_float(cu[j >> 2], j & 3) * fu;
@@ -135,10 +150,19 @@ __global__ __launch_bounds__(256) void swiglu_bwd_q8_kernel(const int8_t* __rest
         *reinterpret_cast<u16x8*>(act + s * I + c) = a8;
         *reinterpret_cast<u16x8*>(d_pre + s * 2 * I + c) = dg8;
         *reinterpret_cast<u16x8*>(d_pre + s * 2 * I + I + c) = du8;
-    }
 #pragma unroll
-    for (int o = kWave / 2; o >= 1; o >>= 1) dp += __shfl_xor(dp, o);
-    if (lane == 0) d_prob[s] = dp;
+        for (int o = 4; o >= 1; o >>= 1) dp += __shfl_xor(dp, o);
+        if ((threadIdx.x & 7) == 0) s_dp[i / 8] = dp;
+    }
+    __syncthreads();
+    const int r = threadIdx.x / 8, n = pieces / 8;
+    if (r < rows) {
+        float dp = 0.0f;
+        for (int j = threadIdx.x & 7; j < n; j += 8) dp += s_dp[r * n + j];
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) dp += __shfl_xor(dp, o);
+        if ((threadIdx.x & 7) == 0) d_prob[row0 + r] = dp;
+    }
 }
 
 int check_pieces(int64_t rows, int32_t cols, std::initializer_list<const void*> ptrs, int64_t* items) {
@@ -213,7 +237,8 @@ extern "C" int moe_swiglu_bwd_q8(const int8_t* codes, const uint8_t* scales, con
         if (!q) return MOE_ERR_INVALID_ARG;
         if (!aligned16(q)) return MOE_ERR_MISALIGNED;
     }
-    swiglu_bwd_q8_kernel<<<static_cast<unsigned>((R + 3) / 4), 256, 0, stream>>>(
-        codes, scales, d_act, slot_probs, static_cast<int>(R), I, act, d_preact, d_prob);
+    const int per = std::max(1, kBwdThreads / (I / 8));
+    swiglu_bwd_q8_kernel<<<static_cast<unsigned>((R + per - 1) / per), kBwdThreads, 0, stream>>>(
+        codes, scales, d_act, slot_probs, static_cast<int>(R), I, per, act, d_preact, d_prob);
     return launch_status();
 }
