@@ -12,10 +12,7 @@
 //     (exact: a 2-bit significand times a power of two) in one instruction,
 //     half a vector instruction per weight.
 //   * The products are 16x16x32 bf16 MFMAs with 16 weight rows as the first
-//     operand and up to 16 routes as the second.  A contraction may run over
-//     its columns in any order that both operands share: a 16-byte piece of
-//     codes is one scale group of a row, and a lane's two pieces of a 256-wide
-//     step feed eight MFMAs as they come.
+//     operand and up to 16 routes as the second.
 //   * A row's scale bytes are loaded for 2048 columns at once and kept in LDS.
 //     Loaded step by step, 8 bytes of each of 64 rows, they took a quarter of
 //     the time (a wide layer's FC1 266 us against 186 without them, 174 now).
@@ -30,7 +27,8 @@
 //     the block's row count and tokens are.
 //
 // One token of a layer of 128 experts (8 a token, H 2048, I 768): FC1 6.1 us,
-// FC2 3.7 us; 16 tokens 33 + 16 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights.
+// FC2 3.7 us; 16 tokens 30 + 15 us; 128 tokens 44 + 26 us, 4.6 TB/s of weights
+// (a plain read of as many bytes: 34 + 18 us).
 #include <algorithm>
 #include <initializer_list>
 
@@ -82,17 +80,17 @@ __device__ __forceinline__ bf16x8 w4_values(uint32_t word, float scale) {
     return r;
 }
 
-// One 256-wide step of one 16-row weight tile against CT column tiles.  Lane
-// (r16, q) holds the codes of columns 64q .. 64q+63 of its row, 8 a word; any
-// order of the contraction will do that both operands share, so the i-th MFMA
-// takes every lane group's i-th word, and the other operand's lanes columns
-// 64q + 8i .. +7 of their rows.  sc: the lane's two scale bytes.
+// Half a 256-wide step of one 16-row weight tile against CT column tiles.  The
+// codes of columns 64q + 32h .. +31 of its row are one 16-byte piece and one
+// scale group of lane (r16, q), 8 columns a word; any order of the contraction
+// will do that both operands share, so the i-th MFMA takes every lane's i-th
+// word, and the other operand's lanes the same columns of their rows.
 template <int CT>
-__device__ __forceinline__ void w4_step(const u32x4 (&cw)[2], uint32_t sc, const u32x4 (&xw)[CT][8], floatx4 (&acc)[CT]) {
+__device__ __forceinline__ void w4_piece(u32x4 codes, uint32_t scale_byte, const u32x4 (&xw)[CT][4], floatx4 (&acc)[CT]) {
+    const float scale = __uint_as_float(scale_byte << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float scale = __uint_as_float((sc >> (8 * (i >> 2)) & 255u) << 23);
-        const bf16x8 a = w4_values(cw[i >> 2][i & 3], scale);
+    for (int i = 0; i < 4; ++i) {
+        const bf16x8 a = w4_values(codes[i], scale);
 #pragma unroll
         for (int c = 0; c < CT; ++c)
             acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, xw[c][i]), acc[c], 0, 0, 0);
@@ -214,9 +212,10 @@ struct W4Rows {
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    // The lane's two scale bytes of tile t, at step k of a panel that starts at kp.
-    __device__ __forceinline__ uint32_t scale_pair(int t, int k, int kp) const {
-        return *reinterpret_cast<const uint16_t*>(s_scale + (t * 16 + r16) * kW4Pitch + (k - kp) * 8 + q * 2);
+    // The scale byte of half h of the lane's columns of tile t, at step k of a
+    // panel that starts at kp.
+    __device__ __forceinline__ uint32_t scale_byte(int t, int k, int kp, int h) const {
+        return s_scale[(t * 16 + r16) * kW4Pitch + (k - kp) * 8 + q * 2 + h];
     }
 
     // Output tile t of one route: the lane's 4 columns col0 + 16t + 4q .. +3,
@@ -282,19 +281,21 @@ struct W4Split : W4Rows<FC1, WT, SALIGN> {
                 if (k == kp) this->load_scales(k);
                 load_codes(k);
             }
-            u32x4 xw[CT][8];
+            u32x4 xw[2][CT][4];
             const bool live = k * kW4Step + q * 64 < p.Kdim;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    xw[c][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    xw[i / 4][c][i % 4] = __builtin_amdgcn_raw_buffer_load_b128(
                         this->rows, live ? aoff[c] + k * (kW4Step * 2) + i * 16 : kOob, 0, 0);
             // every load of the step is issued before the first result is waited for
             __builtin_amdgcn_sched_barrier(0);
             if (k == kp) this->store_scales(k);
 #pragma unroll
-            for (int t = 0; t < WT; ++t) w4_step<CT>(cw[t], this->scale_pair(t, k, kp), xw, acc[t]);
+            for (int t = 0; t < WT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w4_piece<CT>(cw[t][h], this->scale_byte(t, k, kp, h), xw[h], acc[t]);
         }
         // the parts meet in LDS, in the place of the scale panels
         __syncthreads();
@@ -368,7 +369,8 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
 // through LDS into operand layout (16-byte pieces, swizzled by row: no bank
 // conflicts), and the next step's loads run beside this step's products.
 // 128 tokens of the 128-expert layer: FC1 44 us (52 straight to registers),
-// FC2 27 us (32).
+// FC2 26 us (32).  Two steps' loads on their way, 64-row waves, eight waves a
+// workgroup and several column tiles a workgroup in turn were no faster.
 template <bool FC1, int WT, bool SALIGN>
 struct W4Stream : W4Rows<FC1, WT, SALIGN> {
     typedef W4Rows<FC1, WT, SALIGN> B;
@@ -388,7 +390,7 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
     }
 
     template <int CT>
-    __device__ __forceinline__ void run(int c0, bool fetched) {
+    __device__ __forceinline__ void run(int c0, const int (*tok)[2], bool fetched) {
         // the wave brings 4 rows of each 16-row tile, two a load, 512 bytes each
         uint32_t aoff[CT][2];
 #pragma unroll
@@ -396,7 +398,7 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int i = c0 + c * 16 + 4 * wave + 2 * j + lane / 32;
-                aoff[c][j] = this->row_offset(i, FC1 && i < n ? p.sorted_slot_ids[this->slot0 + i] : -1, lane % 32 * 16);
+                aoff[c][j] = this->row_offset(i, tok[c][j], lane % 32 * 16);
             }
         u32x4 xr[CT][2];
         auto load_rows = [&](int k) {
@@ -443,12 +445,6 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
             }
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();                            // the rows are there
-            u32x4 xw[CT][8];
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    xw[c][i] = *reinterpret_cast<const u32x4*>(s_rows + c * 8192 + r16 * 512 + ((q * 8 + i) ^ r16) * 16);
             // past a part's last step: its sums join the total
             while (part < kW4Parts - 1 && k >= w4_part(steps, part + 1)) {
                 ++part;
@@ -461,12 +457,21 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
                     }
             }
 #pragma unroll
-            for (int t = 0; t < WT; ++t) {
-                u32x4 cw[2];
+            for (int h = 0; h < 2; ++h) {               // half a step at a time: its operands in registers
+                u32x4 xw[CT][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    cw[h] = *reinterpret_cast<const u32x4*>(s_codes + (t * 16 + r16) * 128 + ((q * 2 + h) ^ (r16 / 2 % 8)) * 16);
-                w4_step<CT>(cw, this->scale_pair(t, k, kp), xw, acc[t]);
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        xw[c][i] = *reinterpret_cast<const u32x4*>(
+                            s_rows + c * 8192 + r16 * 512 + ((q * 8 + h * 4 + i) ^ r16) * 16);
+#pragma unroll
+                for (int t = 0; t < WT; ++t) {
+                    const u32x4 cw = *reinterpret_cast<const u32x4*>(
+                        s_codes + (t * 16 + r16) * 128 + ((q * 2 + h) ^ (r16 / 2 % 8)) * 16);
+                    w4_piece<CT>(cw, this->scale_byte(t, k, kp, h), xw, acc[t]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
@@ -477,14 +482,23 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
     }
 };
 
+// With one route tile the registers of four waves a SIMD do (16 tokens: FC1 30 us
+// against 33 with the three that the compiler takes unasked); with two they
+// would spill.
 template <bool FC1, int WT, int CTMAX, bool SALIGN>
-__global__ __launch_bounds__(kW4Waves * kWave) void w4_stream_kernel(W4Args p) {
+__global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 1) void w4_stream_kernel(W4Args p) {
     typedef W4Stream<FC1, WT, SALIGN> Wave;
     constexpr int SCALE = Wave::ROWS * kW4Pitch, CODES = Wave::ROWS * 128, ROWS = CTMAX * 8192;
     __shared__ __attribute__((aligned(256))) uint8_t smem[ROWS + kW4Waves * (CODES + SCALE)];
     Wave w(p);
     const int b = blockIdx.y;                           // < R / BM
     w.slot0 = b * kBlockM;
+    int tok[2][2];                                      // of the rows that the wave brings
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            tok[c][j] = FC1 ? p.sorted_slot_ids[w.slot0 + c * 16 + 4 * w.wave + 2 * j + w.lane / 32] : 0;
     const int e = p.expert_ids[b];                      // device data: range-checked
     if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) return;      // past the extent
     w.s_rows = smem;
@@ -499,15 +513,15 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_stream_kernel(W4Args p) {
     __builtin_amdgcn_sched_barrier(0);
     if (!w.routes(b, e)) return;                        // uniform over the workgroup
     if (CTMAX == 1) {
-        w.template run<1>(0, true);
+        w.template run<1>(0, tok, true);
         if (w.n > 16) {
             __syncthreads();                            // the last step's rows are read
-            w.template run<1>(16, false);
+            w.template run<1>(16, tok + 1, false);
         }
     } else if (w.n <= 16) {
-        w.template run<1>(0, true);
+        w.template run<1>(0, tok, true);
     } else {
-        w.template run<CTMAX>(0, true);
+        w.template run<CTMAX>(0, tok, true);
     }
 }
 
