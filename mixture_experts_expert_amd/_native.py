@@ -810,8 +810,8 @@ def moe_gather_combine_f32(route_out, token_routes, y, stream=None):
 def moe_grouped_ffn_w4(x, w1_codes, w1_scales, w2_codes, w2_scales, sorted_slot_ids, slot_probs,
                        expert_ids, block_start, route_counts, token_routes, act, route_out, y,
                        stream=None):
-    """Steps 4-5 of the dropless form on 4-bit weights: FC1 + SwiGLU * prob into act, FC2 into
-    route_out (float32), each token's sum into y."""
+    """Steps 4-5 of the dropless form on 4-bit weights: FC1 + SwiGLU * prob, FC2 and each token's
+    sum into y.  act [R, I] and route_out [R, H] (float32) are scratch."""
     dev, st = _here_of(x, "x", stream)
     N, H = x.shape
     n, K = token_routes.shape

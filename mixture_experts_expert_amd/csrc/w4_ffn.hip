@@ -26,8 +26,8 @@
 //   * The weights' first loads leave as soon as the expert is known, before
 //     the block's row count and tokens are.
 //
-// One token of a layer of 128 experts (8 a token, H 2048, I 768): FC1 6.1 us,
-// FC2 3.7 us; 16 tokens 30 + 15 us; 128 tokens 44 + 26 us, 4.6 TB/s of weights
+// One token of a layer of 128 experts (8 a token, H 2048, I 768): 13.3 us, FC1
+// 6.1 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 26 us, 4.6 TB/s of weights
 // (a plain read of as many bytes: 34 + 18 us).
 #include <algorithm>
 #include <initializer_list>
@@ -525,6 +525,68 @@ __global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 1) void w4_strea
     }
 }
 
+// ------------------------------------------------------------ a few tokens
+// FC2 and the token's sum in one launch: workgroup (x, y) forms 16 columns of
+// y[token y].  Its waves share out the token's K routes times the parts of the
+// contraction; a part's sums of 16 columns go to LDS, and 16 threads add them,
+// parts in order to a route's row, routes in k order to the token's: the
+// additions of the kernels above and of combine_f32_kernel, without the pass
+// through route_out.  Every token reads its own experts, and most columns of
+// the second operand are empty.
+constexpr int kW4TokenWaves = 8;
+
+__global__ __launch_bounds__(kW4TokenWaves * kWave) void w4_fc2_token_kernel(W4Args p,
+                                                                             const int* __restrict__ token_routes,
+                                                                             int K, uint16_t* __restrict__ y) {
+    __shared__ __attribute__((aligned(16))) float s_sum[kMaxK * kW4Parts][16];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    const int r16 = lane & 15, q = lane >> 4;
+    const int col0 = blockIdx.x * 16;                   // ncols is a multiple of 16
+    const int64_t t = blockIdx.y;
+    const int steps = (p.Kdim + kW4Step - 1) / kW4Step, sbytes = p.Kdim / kGroup;
+    for (int i = wave; i < K * kW4Parts; i += kW4TokenWaves) {
+        const int slot = token_routes[t * K + i / kW4Parts], part = i % kW4Parts;
+        int e = -1;                                     // device data: range-checked
+        if (static_cast<unsigned>(slot) < static_cast<unsigned>(p.R)) e = p.expert_ids[slot / kBlockM];
+        floatx4 acc[1] = {floatx4{0.0f, 0.0f, 0.0f, 0.0f}};
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(p.E)) {
+            const int64_t base = static_cast<int64_t>(e) * p.wrows + col0;
+            const __amdgpu_buffer_rsrc_t codes = buffer(p.codes + base * (p.Kdim / 2), 16u * (p.Kdim / 2));
+            const __amdgpu_buffer_rsrc_t scales = buffer(p.scales + base * sbytes, 16u * sbytes);
+            const __amdgpu_buffer_rsrc_t row = buffer(p.a + static_cast<int64_t>(slot) * p.Kdim, p.Kdim * 2u);
+            for (int s = w4_part(steps, part); s < w4_part(steps, part + 1); ++s) {
+                const bool live = s * kW4Step + q * 64 < p.Kdim;   // past the row's end: zeros
+                u32x4 cw[2], xw[2][1][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    cw[h] = __builtin_amdgcn_raw_buffer_load_b128(
+                        codes, live ? r16 * (p.Kdim / 2) + s * (kW4Step / 2) + q * 32 + h * 16 : kOob, 0, 0);
+                const uint32_t sc = __builtin_amdgcn_raw_buffer_load_b16(
+                    scales, live ? r16 * sbytes + s * (kW4Step / kGroup) + q * 2 : kOob, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)             // the route is the first of 16 columns, the others zeros
+                    xw[j / 4][0][j % 4] = __builtin_amdgcn_raw_buffer_load_b128(
+                        row, live && r16 == 0 ? s * (kW4Step * 2) + q * 128 + j * 16 : kOob, 0, 0);
+                w4_piece<1>(cw[0], sc & 255u, xw[0], acc);
+                w4_piece<1>(cw[1], sc >> 8, xw[1], acc);
+            }
+        }
+        if (r16 == 0) *reinterpret_cast<floatx4*>(&s_sum[i][4 * q]) = acc[0];
+    }
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        float v = 0.0f;
+        for (int k = 0; k < K; ++k) {
+            float r = s_sum[k * kW4Parts][threadIdx.x];
+#pragma unroll
+            for (int i = 1; i < kW4Parts; ++i) r += s_sum[k * kW4Parts + i][threadIdx.x];
+            v += r;
+        }
+        y[t * p.ncols + col0 + threadIdx.x] = f32_to_bf16(v);
+    }
+}
+
 // y[t] = bf16( sum over k, from +0.0 in k order, of the token's routes ).
 // Workgroup (x, y): 1024 columns of token y, 4 a thread; the token's routes are
 // uniform, so all K rows are on their way after one scalar load.
@@ -562,6 +624,15 @@ void launch_combine_f32(const float* ro, const int* tr, int N, int K, int H, int
 int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
     const int64_t routes = N * K;
     return static_cast<int>(std::min<int64_t>(R, routes + (kBlockM - 1) * std::min<int64_t>(E, routes)) / kBlockM);
+}
+
+// Whether FC2 and the combine run in one launch, token by token: while that
+// reads at most 32 MB of codes (an expert is read by every token that picks
+// it).  One token of the 128-expert layer takes 13.3 us instead of 15.2, 4 take
+// 21.6 instead of 25.3, 3 of a small layer 6.7 instead of 8.4; 8 (50 MB) and one
+// of a wide layer (59 MB) are slower by 6%.
+bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {
+    return N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(32) << 20;
 }
 
 int check_w4(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K, int64_t* R) {
@@ -647,6 +718,11 @@ int ffn_w4(int which, const uint16_t* x, const uint8_t* w1_codes, const uint8_t*
     if (which & 2) {
         a.a = act; a.codes = w2_codes; a.scales = w2_scales;
         a.out = route_out; a.Kdim = I; a.ncols = H; a.wrows = H;
+        if (which == 7 && w4_by_token(N, H, I, K)) {
+            w4_fc2_token_kernel<<<dim3(H / 16, static_cast<unsigned>(N)), kW4TokenWaves * kWave, 0, stream>>>(
+                a, token_routes, K, y);
+            return launch_status();
+        }
         dispatch_w4<false>(a, blocks, mean, stream);
     }
     if (which & 4) return moe_gather_combine_f32(route_out, token_routes, N, K, H, R, y, stream);
