@@ -110,7 +110,7 @@ int moe_gather_combine_f32(const float* route_out, const int32_t* token_routes, 
 /* The three calls above, in order, on one stream: the same y, bit for bit.
  * act and route_out are scratch here: what they hold afterwards is unspecified
  * (for a few tokens FC2 and the sum run as one kernel, which leaves route_out
- * alone). */
+ * alone), and calls that share them must not overlap. */
 int moe_grouped_ffn_w4(const uint16_t* x, const uint8_t* w1_codes, const uint8_t* w1_scales,
                        const uint8_t* w2_codes, const uint8_t* w2_scales,
                        const int32_t* sorted_slot_ids, const float* slot_probs,

@@ -56,7 +56,6 @@ struct FfnArgs {
     const float* slot_probs;      // FC1 only
     uint16_t* out;                // FC1: act [E*Cp, I]; FC2: route_out [E*Cp, H]
     void* preact;                 // FC1 only, may be null: raw [gate | up] [E*Cp, 2I], bf16 or (scales) int8 codes
-    uint8_t* scales;              // the codes' scale bytes [E*Cp, 2I/32], or null
     int N;                        // tokens (FC1 sentinel row)
     int Kdim;                     // contraction length: FC1 H, FC2 I
     int ncols;                    // output columns: FC1 I, FC2 H
@@ -71,6 +70,7 @@ struct FfnArgs {
     const int* extent;
     int E;
     int R;                        // slots of the route list (its static bound)
+    uint8_t* scales;              // FC1 only, may be null: preact holds int8 codes, these their scale bytes [E*Cp, 2I/32]
 };
 
 // One persistent workgroup per resident slot walks the tiles r*G + slot

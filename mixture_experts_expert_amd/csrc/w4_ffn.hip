@@ -26,7 +26,7 @@
 //   * The weights' first loads leave as soon as the expert is known, before
 //     the block's row count and tokens are.
 //
-// One token of a layer of 128 experts (8 a token, H 2048, I 768): 13.3 us, FC1
+// One token of a layer of 128 experts (8 a token, H 2048, I 768): 11.9 us, FC1
 // 6.1 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 26 us, 4.6 TB/s of weights
 // (a plain read of as many bytes: 34 + 18 us).
 #include <algorithm>
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 1) void w4_strea
 // additions of the kernels above and of combine_f32_kernel, without the pass
 // through route_out.  Every token reads its own experts, and most columns of
 // the second operand are empty.
-constexpr int kW4TokenWaves = 8;
+constexpr int kW4TokenWaves = 16;
 
 __global__ __launch_bounds__(kW4TokenWaves * kWave) void w4_fc2_token_kernel(W4Args p,
                                                                              const int* __restrict__ token_routes,
@@ -628,7 +628,7 @@ int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
 
 // Whether FC2 and the combine run in one launch, token by token: while that
 // reads at most 32 MB of codes (an expert is read by every token that picks
-// it).  One token of the 128-expert layer takes 13.3 us instead of 15.2, 4 take
+// it).  One token of the 128-expert layer takes 11.9 us instead of 15.2, 4 take
 // 21.6 instead of 25.3, 3 of a small layer 6.7 instead of 8.4; 8 (50 MB) and one
 // of a wide layer (59 MB) are slower by 6%.
 bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {

@@ -132,6 +132,11 @@ SHAPES = {
     "stream_odd_scales": (60, 1088, 1344, 48, 8),
     "stream_long": (40, 4160, 1536, 48, 4),
     "split_long": (3, 4160, 2112, 4, 2),
+    # the longest contraction, in whole steps and ending inside one: two panels
+    # of scales a wave of the split kernel
+    "longest": (2, 16384, 64, 2, 1),
+    "longest_odd": (2, 16320, 64, 2, 1),
+    "longest_fc2": (2, 64, 16384, 2, 1),
 }
 
 

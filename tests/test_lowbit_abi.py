@@ -138,3 +138,31 @@ def test_signatures_take_as_many_arguments_as_declared():
         args = re.search(r"\b%s\s*\((.*?)\)\s*;" % n, text, flags=re.S).group(1)
         assert len(args.split(",")) == len(nat._SIGNATURES[n][1]), n
     assert nat._SIGNATURES["moe_grouped_ffn_w4"][0] is ctypes.c_int
+
+
+def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
+    class Elsewhere(torch.Tensor):            # a tensor that says it lives on cuda:1
+        is_cuda = True
+        device = torch.device("cuda:1")
+
+        def get_device(self):
+            return 1
+
+    t = torch.zeros(8).as_subclass(Elsewhere)
+    assert nat._at(t, torch.float32, 8, "t", 1) == t.data_ptr()
+    with pytest.raises(ValueError, match="t is on cuda:1, the current device is cuda:0"):
+        nat._at(t, torch.float32, 8, "t", 0)
+    with pytest.raises(ValueError, match="at least 9"):
+        nat._at(t, torch.float32, 9, "t", 1)
+    with pytest.raises(TypeError, match="expected torch.int32"):
+        nat._at(t, torch.int32, 8, "t", 1)
+
+    class Stream:
+        device_index, cuda_stream = 1, 1234
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="stream is on device 1"):
+        nat._here(Stream())
+    Stream.device_index = 0
+    assert nat._here(Stream()) == (0, 1234)
+    assert nat._here(77) == (0, 77)
