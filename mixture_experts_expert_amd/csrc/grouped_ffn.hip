@@ -859,6 +859,29 @@ int pick_tile_m(int Cp) {
     return best;
 }
 
+// M-tile of the FC1 that saves 8-bit codes: the one with the least time, as the
+// rounds its tiles make over the resident workgroups (two a compute unit for
+// 32 and 64 rows, one for the larger) times a round's time, which goes with
+// the contraction's length alone.  Measured on 24 experts of 32 .. 2752 slots
+// (H 1536, I 768), a round takes 27, 29, 31, 44 and 58 us with 32, 64, 128,
+// 256 and 320 rows, and the counts of rounds explain the times: 544 slots run
+// 87 us in 256-row tiles where the least padding would take 32-row ones and
+// 243, 160 slots 45 against 80, 96 slots 36 against 54.  (Every tile gives the
+// same bits.)
+int pick_tile_rounds(int E, int Cp, int I) {
+    const struct { int rows, cols, resident, cost; } shapes[] = {
+        {32, 64, 2, 27}, {64, 64, 2, 29}, {128, 128, 1, 31}, {256, 128, 1, 44}, {320, 128, 1, 58}};
+    int best = 256;
+    int64_t best_time = INT64_MAX;
+    for (const auto& t : shapes) {
+        const int64_t tiles = static_cast<int64_t>(E) * ((Cp + t.rows - 1) / t.rows) * ((I + t.cols - 1) / t.cols);
+        const int64_t slots = static_cast<int64_t>(device_cus()) * t.resident;
+        const int64_t time = (tiles + slots - 1) / slots * t.cost;
+        if (time < best_time) { best = t.rows; best_time = time; }
+    }
+    return best;
+}
+
 // Variable segments: every row tile of an expert streams its weight panel
 // (from HBM or, beside a sibling tile, from L2), so the tile should hold a
 // typical segment whole.  With routes spread evenly a segment holds about
@@ -908,7 +931,7 @@ int launch(const FfnArgs& a, bool fc1, int E, hipStream_t s, bool dyn = false, d
         // steps the cross-tile look-ahead needs
         return launch_gemm<32, 128, 1, 2, 32, 2, 3>(a, fc1, E, s, dyn);
     }
-    switch (dyn ? pick_tile_dyn(mean) : pick_tile_m(a.Cp)) {
+    switch (dyn ? pick_tile_dyn(mean) : a.scales ? pick_tile_rounds(E, a.Cp, a.ncols) : pick_tile_m(a.Cp)) {
         // 64-wide K slabs (128 contiguous bytes per weight row per step keep the
         // HBM stream efficient); rings sized to the 160 KB LDS.
         case 320: return launch_gemm<320, 256, 2, 4, 64, 2, 2>(a, fc1, E, s, dyn);

@@ -137,6 +137,10 @@ SAVE = {
     "c320": (640, 192, 448, 4, 2, 1.0),
     "c352_pads": (512, 128, 128, 4, 2, 1.375),
     "drops": (700, 192, 192, 6, 3, 0.6),
+    # many tiles: the larger row tiles, ending inside a segment
+    "many_c544": (2176, 128, 704, 32, 8, 1.0),
+    "many_c320": (1280, 192, 768, 32, 8, 1.0),
+    "many_c96": (768, 256, 512, 64, 8, 1.0),
 }
 
 
