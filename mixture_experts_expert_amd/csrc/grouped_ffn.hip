@@ -105,8 +105,9 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
     // stores per lane per tile (FC1 with SAVE also stores the raw gate and up
     // columns, the pre-activation the backward keeps: 1 as bf16, two more
     // 16-byte stores a block; 2 as 8-bit codes, one 16-byte store of gate and
-    // of up codes and one scale byte a row block)
-    constexpr int STORES = FC1 ? (SAVE == 1 ? 3 : 1) * MI * NI + (SAVE == 2 ? 3 * MI : 0) : 2 * MI * NI;
+    // of up codes a row block, and the scale bytes: one a row block straight
+    // from the registers, one or two stores for the staged tile)
+    constexpr int STORES = FC1 ? (SAVE == 1 ? 3 : 1) * MI * NI + (SAVE == 2 ? 2 * MI + (EPI ? 1 : MI) : 0) : 2 * MI * NI;
     static_assert(FC1 || !SAVE, "only FC1 has a pre-activation");
     static_assert(SAVE != 2 || NI == 2, "a wave's 32 gate columns are one scale group");
     constexpr int LDS_BYTES = NA * A_STAGE + NB * B_STAGE;
@@ -518,8 +519,8 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
         // up's in the upper, which takes that group's scale byte; another hands
         // both factors to both.  The codes of the lane's 16 columns, half*16 ..
         // of the wave's 32, come out as one 16-byte piece of gate and of up.
-        // Stores the scale byte.
-        auto fc1_q8 = [&](int mi, u32x4 (&codes)[2]) {
+        // Returns the lane's scale byte (lower lanes gate, upper lanes up).
+        auto fc1_q8 = [&](int mi, u32x4 (&codes)[2]) -> int {
             uint32_t m[2] = {0, 0};
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
@@ -550,12 +551,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                 codes[part][0] = s0[0]; codes[part][1] = s0[1];
                 codes[part][2] = s1[0]; codes[part][3] = s1[1];
             }
-            const int row = cur.m0 + wm * WTM + mi * 32 + (lane & 31);
-            const int col = cur.nt * OUT_COLS + wn * WTN / 2;   // the wave's first column: a whole group
-            __builtin_amdgcn_raw_buffer_store_b8(
-                static_cast<uint8_t>(b), srsrc,
-                row < cur.len && col < p.ncols
-                    ? static_cast<uint32_t>(row) * srow + (col + half * p.ncols) / kGroup : kOob, 0, 0);
+            return b;
         };
         // FC1: the lane's 8 activations of block (mi, ni), tile columns
         // (wn*WTN + ni*32)/2 + 8*half ..
@@ -626,6 +622,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                     return d;
                 };
                 bool started = false;
+                uint8_t sbyte[SAVE == 2 ? MI : 1];
 #pragma unroll
                 for (int part = 0; part < (SAVE == 1 ? 3 : SAVE == 2 ? 2 : 1); ++part) {
 #pragma unroll
@@ -638,7 +635,7 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                             if (r0 < base || r0 >= base + CAP) continue;
                             if (SAVE == 2 && part == 1) {
                                 u32x4 codes[2];
-                                fc1_q8(mi, codes);
+                                sbyte[SAVE == 2 ? mi : 0] = static_cast<uint8_t>(fc1_q8(mi, codes));
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     *(lds_u32x4*)((lds_u8*)smem + so(r0 - base + (lane & 31), h * 8 + wn * 2 + half)) =
@@ -675,6 +672,29 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                                 __builtin_amdgcn_raw_buffer_store_b128(v, prsrc, live ? poff : kOob, 0, POLICY);
                             }
                         }
+                    }
+                }
+                if constexpr (SAVE == 2) {
+                    // the scale bytes, 4 of gate and 4 of up a row, meet in LDS too:
+                    // a byte at a time from the four waves of a row they took 3 to
+                    // 10 us of 150 to 220
+                    static_assert(BMT == 256 && NW * kWave == 2 * BMT, "two threads a row");
+                    __syncthreads();                       // the codes are read back
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi)
+                        smem[rA + (wm * WTM + mi * 32 + (lane & 31)) * 8 + half * 4 + wn] = sbyte[mi];
+                    __syncthreads();
+                    const int sr = threadIdx.x / 2, up = threadIdx.x & 1;
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(smem + rA + sr * 8 + up * 4);
+                    const int row = cur.m0 + sr, col = cur.nt * OUT_COLS;
+                    const uint32_t off = static_cast<uint32_t>(row) * srow + (col + up * p.ncols) / kGroup;
+                    if (p.ncols % OUT_COLS == 0) {
+                        __builtin_amdgcn_raw_buffer_store_b32(v, srsrc, row < cur.len ? off : kOob, 0, 0);
+                    } else {                               // whole pairs: columns are a multiple of 64
+                        __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v), srsrc, row < cur.len ? off : kOob, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            static_cast<uint16_t>(v >> 16), srsrc,
+                            row < cur.len && col + 64 < p.ncols ? off + 2 : kOob, 0, 0);
                     }
                 }
             } else {
@@ -764,8 +784,13 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
                 }
                 if constexpr (SAVE == 2) {
                     u32x4 codes[2];
-                    fc1_q8(mi, codes);
-                    const int col = cur.nt * OUT_COLS + wn * WTN / 2 + 16 * half;
+                    const int sb = fc1_q8(mi, codes);
+                    const int col0 = cur.nt * OUT_COLS + wn * WTN / 2;   // the wave's first: a whole group
+                    __builtin_amdgcn_raw_buffer_store_b8(
+                        static_cast<uint8_t>(sb), srsrc,
+                        row < cur.len && col0 < p.ncols
+                            ? static_cast<uint32_t>(row) * srow + (col0 + half * p.ncols) / kGroup : kOob, 0, 0);
+                    const int col = col0 + 16 * half;
                     const uint32_t qoff = row < cur.len && col < p.ncols
                         ? static_cast<uint32_t>(row) * 2u * p.ncols + col : kOob;
                     __builtin_amdgcn_raw_buffer_store_b128(codes[0], prsrc, qoff, 0, 0);

@@ -140,7 +140,13 @@ SAVE = {
     # many tiles: the larger row tiles, ending inside a segment
     "many_c544": (2176, 128, 704, 32, 8, 1.0),
     "many_c320": (1280, 192, 768, 32, 8, 1.0),
-    "many_c96": (768, 256, 512, 64, 8, 1.0),
+    # enough tiles for each row tile: 64, 128, 256 (whole, and ending inside in
+    # rows and columns), 320
+    "tile64": (768, 128, 768, 24, 2, 1.0),
+    "tile128": (768, 256, 512, 64, 8, 1.0),
+    "tile256": (4096, 128, 256, 128, 8, 1.0),
+    "tile256_ragged": (3500, 192, 320, 128, 8, 1.0),
+    "tile320": (5120, 128, 256, 128, 8, 1.0),
 }
 
 
@@ -169,7 +175,8 @@ def test_fc1_save_q8(name):
     torch.cuda.synchronize()
     assert torch.equal(act[:R], ref), "act differs from the plain forward's"
     assert bool((codes[R:] == 77).all()) and bool((scales[R:] == 77).all()) and bool((act[R:] == 7).all())
-    check_checkpoint(buf, host(x), host(w1), host(codes)[:R], host(scales)[:R])
+    check_checkpoint(buf, host(x), host(w1), host(codes)[:R], host(scales)[:R],
+                     range(0, E, 1 if E <= 64 else 9))
 
 
 def check_checkpoint(buf, x, w1, codes, b, experts=None):
