@@ -33,6 +33,10 @@
 //     into the two LDS stages its last K step freed and goes out in whole
 //     128-byte lines, which disturbs the load stream far less than 32-byte
 //     pieces straight from the accumulator layout;
+//   * FC1 can keep its pre-activation, in bf16 or in 8 bits with a scale byte
+//     per 32 columns: quantized from the accumulators, it leaves through the
+//     staged tile too and is 52% of the bf16 bytes (4096 tokens, 128 experts,
+//     8 a token, H 2048, I 768: 201 us without, 211 in 8 bits, 216 in bf16);
 //   * FC2 with an output row map (an expert-parallel rank's return layout)
 //     runs on the producer/consumer slot GEMM (slot_gemm.h).
 #include <algorithm>
@@ -521,15 +525,15 @@ __global__ __launch_bounds__(WM * WN * kWave) void ffn_gemm_kernel(FfnArgs p) {
         // of the wave's 32, come out as one 16-byte piece of gate and of up.
         // Returns the lane's scale byte (lower lanes gate, upper lanes up).
         auto fc1_q8 = [&](int mi, u32x4 (&codes)[2]) -> int {
-            uint32_t m[2] = {0, 0};
+            float m[2] = {0.0f, 0.0f};                      // a NaN is kept: half an instruction an element
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    m[0] = max(m[0], abs_bits(acc[mi][ni][j]));
-                    m[1] = max(m[1], abs_bits(acc[mi][ni][8 + j]));
+                    m[0] = __builtin_elementwise_maximum(m[0], __builtin_fabsf(acc[mi][ni][j]));
+                    m[1] = __builtin_elementwise_maximum(m[1], __builtin_fabsf(acc[mi][ni][8 + j]));
                 }
-            const auto mm = __builtin_amdgcn_permlane32_swap(m[0], m[1], false, false);
+            const auto mm = __builtin_amdgcn_permlane32_swap(abs_bits(m[0]), abs_bits(m[1]), false, false);
             const int b = q8_scale_byte(max(mm[0], mm[1]));
             const uint32_t iv = __float_as_uint(inv_scale(b));
             const auto ii = __builtin_amdgcn_permlane32_swap(iv, iv, false, false);

@@ -38,11 +38,13 @@ __device__ __forceinline__ float inv_scale(int b) {
 // number (ties to even) in the low mantissa bits, one rounding in the fma.
 // (inf and NaN times inv = 0 are NaN, whose low byte is masked by the caller.)
 __device__ __forceinline__ uint32_t q8_code(float v, float inv) {
-    return __float_as_uint(__builtin_fmaf(v, inv, 12582912.0f)) & 0xFFu;
+    return __float_as_uint(__builtin_fmaf(v, inv, 12582912.0f));
 }
 
+// Four codes as the bytes of a word.
 __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d, float inv) {
-    return q8_code(a, inv) | q8_code(b, inv) << 8 | q8_code(c, inv) << 16 | q8_code(d, inv) << 24;
+    return __builtin_amdgcn_perm(q8_code(b, inv), q8_code(a, inv), 0x0C0C0400u) |
+           __builtin_amdgcn_perm(q8_code(d, inv), q8_code(c, inv), 0x04000C0Cu);
 }
 
 // 2^(b - 127) of a scale byte; a NaN for b = 255.  b = 0 (2^-127, written by
