@@ -626,13 +626,15 @@ int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
     return static_cast<int>(std::min<int64_t>(R, routes + (kBlockM - 1) * std::min<int64_t>(E, routes)) / kBlockM);
 }
 
-// Whether FC2 and the combine run in one launch, token by token: while that
-// reads at most 32 MB of codes (an expert is read by every token that picks
-// it).  One token of the 128-expert layer takes 11.9 us instead of 15.2, 4 take
-// 21.6 instead of 25.3, 3 of a small layer 6.7 instead of 8.4; 8 (50 MB) and one
-// of a wide layer (59 MB) are slower by 6%.
+// Whether FC2 and the combine run in one launch, token by token: while that is
+// at most 1024 workgroups (two rounds of 16 waves over the compute units; 32
+// tokens of a 512-wide layer 7.6 us instead of 8.4, 64 10.2 against 8.6) and
+// reads at most 24 MB of codes (an expert is read by every token that picks
+// it: 8 tokens of 4 experts of 2048 x 768 22.7 us instead of 23.4, of 8
+// experts 41.5 against 40.5).  One token of the 128-expert layer takes 12.4 us
+// instead of 15.7.
 bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {
-    return N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(32) << 20;
+    return N * H <= 1024 * 16 && N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(24) << 20;
 }
 
 int check_w4(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K, int64_t* R) {
@@ -660,12 +662,14 @@ template <bool FC1, int CTMAX>
 void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
     constexpr int threads = kW4Waves * kWave;
     const bool salign = a.Kdim % 128 == 0;
+    const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
+    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (salign ? 3 : 2) && steps <= 4;
     auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
-    if (tiles >= 2000) {
+    if (tiles >= (CTMAX == 1 ? 1200 : 600) && !partial) {
         const dim3 g = grid((FC1 ? 16 : 32) * kW4Waves);
         if (salign) w4_stream_kernel<FC1, 2, CTMAX, true><<<g, threads, 0, s>>>(a);
         else w4_stream_kernel<FC1, 2, CTMAX, false><<<g, threads, 0, s>>>(a);
-    } else if (tiles >= 500) {
+    } else if (tiles >= (CTMAX == 1 ? 500 : steps > 2 ? 165 : 400)) {
         const dim3 g = grid(FC1 ? 32 : 64);
         if (salign) w4_split_kernel<FC1, 4, CTMAX, true><<<g, threads, 0, s>>>(a);
         else w4_split_kernel<FC1, 4, CTMAX, false><<<g, threads, 0, s>>>(a);
@@ -677,13 +681,24 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
 }
 
 // Which kernel: by the most tiles of 64 weight rows that the route list can
-// ask for.  Under 500 (two workgroups a compute unit) the split kernel takes
-// 32-row workgroups, for more of them (3 tokens of a small layer: 8.6 us
-// against 10.0); from 2000 on the streaming one fills the device (128 tokens,
-// 128 experts: 76 us against 83 split; 4 tokens, 768 tiles: 25 us split, 27
-// streaming).  Two 16-route tiles are held at once where experts have more
-// than 10 routes on average (12 a head: 87 us against 92; 8: 80 against 76,
-// the registers of the second tile cost a workgroup a compute unit).
+// ask for.
+//   * Under 500 (two workgroups a compute unit) the split kernel takes 32-row
+//     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows,
+//     498 3.9 with either, 638 4.9 against 4.0), and from 1200 on the streaming
+//     one fills the device (920 tiles of 2 steps 7.1 us against 5.9 split, 1140
+//     of 12 steps 22.2 against 26.7, 1219 of one 4.9 against 5.7).
+//   * The streaming kernel pays for a step that the contraction ends inside of:
+//     with 2 to 4 steps split stays ahead (3404 tiles of 576 columns 14.6 us
+//     against 17.3, of 768 18.9 against 17.2).
+//   * Two 16-route tiles are held at once where experts have more than 10 routes
+//     on average (12 a head: 87 us against 92; 8: 80 against 76, the registers of
+//     the second tile cost a workgroup a compute unit).  The split kernel then
+//     reads twice the operands, and its address units are the time: 64-row
+//     workgroups as soon as 32-row ones are more than one a compute unit (168
+//     tiles of 22 steps 19.5 us against 27.4, 138 of 16 steps 16.1 against 14.5;
+//     with one or two steps later, 300 tiles 4.6 us against 4.5), streaming from
+//     600 (595 of 2 steps 5.6 us against 4.9 split, 663 of one 5.8 against 7.7,
+//     2204 of 5 23 against 32).
 template <bool FC1>
 void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
     const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64));

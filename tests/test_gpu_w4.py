@@ -132,6 +132,14 @@ SHAPES = {
     "stream_odd_scales": (60, 1088, 1344, 48, 8),
     "stream_long": (40, 4160, 1536, 48, 4),
     "split_long": (3, 4160, 2112, 4, 2),
+    # either side of the sizes that choose the kernel: FC2 with the sum or
+    # without, workgroups of 32 or 64 rows, streaming early or late
+    "many_tokens_of_a_small_layer": (257, 64, 64, 12, 1),
+    "tokens_at_the_bound": (256, 64, 64, 12, 1),
+    "split_64_rows_many_rows": (60, 832, 640, 4, 3),
+    "stream_early_many_rows": (120, 768, 1280, 12, 3),
+    "stream_early_few_rows": (42, 512, 1216, 32, 6),
+    "split_steps_end_inside": (64, 1088, 576, 64, 6),
     # the longest contraction, in whole steps and ending inside one: two panels
     # of scales a wave of the split kernel
     "longest": (2, 16384, 64, 2, 1),
