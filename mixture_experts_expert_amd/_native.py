@@ -655,8 +655,9 @@ _capacity = functools.lru_cache(maxsize=4096)(moe_padded_capacity)
 
 def _here(stream):
     """The current device and the stream's handle on it.  Kernels are launched
-    on the current device: a stream of another one is refused."""
-    dev = torch.cuda.current_device()
+    on the current device: a stream of another one is refused.  (A device
+    tensor is at hand, so the device runtime is up.)"""
+    dev = torch._C._cuda_getDevice()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     where = getattr(stream, "device_index", None)
@@ -679,7 +680,8 @@ def _at(t, dtype, numel: int, name: str, dev: int) -> int:
     """Address of a contiguous tensor of `dtype` on device `dev` with at least
     `numel` elements; anything else is refused."""
     try:
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+                and (not numel or t.numel() >= numel)):
             return t.data_ptr()
     except AttributeError:
         pass
