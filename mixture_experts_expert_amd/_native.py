@@ -655,9 +655,8 @@ _capacity = functools.lru_cache(maxsize=4096)(moe_padded_capacity)
 
 def _here(stream):
     """The current device and the stream's handle on it.  Kernels are launched
-    on the current device: a stream of another one is refused.  (A device
-    tensor is at hand, so the device runtime is up.)"""
-    dev = torch._C._cuda_getDevice()
+    on the current device: a stream of another one is refused."""
+    dev = torch.cuda.current_device()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     where = getattr(stream, "device_index", None)
