@@ -26,8 +26,8 @@
 //   * The weights' first loads leave as soon as the expert is known, before
 //     the block's row count and tokens are.
 //
-// One token of a layer of 128 experts (8 a token, H 2048, I 768): 11.9 us, FC1
-// 6.1 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 26 us, 4.6 TB/s of weights
+// One token of a layer of 128 experts (8 a token, H 2048, I 768): 12.0 us, FC1
+// 6.3 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights
 // (a plain read of as many bytes: 34 + 18 us).
 #include <algorithm>
 #include <initializer_list>
