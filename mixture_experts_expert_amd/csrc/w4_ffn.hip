@@ -26,8 +26,8 @@
 //   * The weights' first loads leave as soon as the expert is known, before
 //     the block's row count and tokens are.
 //
-// One token of a layer of 128 experts (8 a token, H 2048, I 768): 12.0 us, FC1
-// 6.3 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights
+// One token of a layer of 128 experts (8 a token, H 2048, I 768): 11.6 us, FC1
+// 5.6 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights
 // (a plain read of as many bytes: 34 + 18 us).
 #include <algorithm>
 #include <initializer_list>
@@ -96,6 +96,10 @@ __device__ __forceinline__ void w4_piece(u32x4 codes, uint32_t scale_byte, const
             acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, xw[c][i]), acc[c], 0, 0, 0);
     }
 }
+
+// A wave's LDS operations are in order; this keeps the compiler from moving
+// reads and writes past each other.
+__device__ __forceinline__ void w4_wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // First step of part i of a contraction of `steps` steps.
 __device__ __forceinline__ int w4_part(int steps, int i) { return steps * i / kW4Parts; }
@@ -194,11 +198,10 @@ struct W4Rows {
                 if (i * 4 < cnt + 2) sv[i] = __builtin_amdgcn_raw_buffer_load_b32(scales, at + i * 4, 0, 0);
         }
     }
-    // The panel is the wave's own: its LDS operations are in order, the fences
-    // keep the compiler from moving reads and writes past each other.
+    // The panel is the wave's own.
     __device__ __forceinline__ void store_scales(int kp) {
         const int cnt = panel_bytes(kp);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        w4_wave_fence();
 #pragma unroll
         for (int i = 0; i < kW4Panel; ++i) {
             u32x2 v;
@@ -210,7 +213,7 @@ struct W4Rows {
             }
             if (lane < ROWS) *reinterpret_cast<u32x2*>(s_scale + lane * kW4Pitch + i * 8) = v;
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        w4_wave_fence();
     }
     // The scale byte of half h of the lane's columns of tile t, at step k of a
     // panel that starts at kp.
@@ -240,27 +243,45 @@ struct W4Rows {
 
 // ---------------------------------------------------------------- few tiles
 // Workgroup (x, y): WT weight tiles and layout block y; wave w sums part w of
-// the contraction.  Every load goes straight to operand registers, the
-// shortest way when a wave has one step or two.  Lane (r16, q) takes the 32
-// bytes of codes of columns 64q .. 64q+63 of its row, and the other operand's
-// lanes those columns of their rows.
-template <bool FC1, int WT, bool SALIGN>
+// the contraction.  Loads go straight to operand registers, the shortest way
+// when a wave has one step.  Lane (r16, q) takes the 32 bytes of codes of
+// columns 64q .. 64q+63 of its row, and the other operand's lanes those columns
+// of their rows.  STAGED: the codes come in whole lines and through LDS of the
+// wave's own (which needs no barrier), for contractions of several steps a wave,
+// where 64 cache accesses a load add up (one token, H 2048: FC1 5.6 us against
+// 6.2, H 6912 17.2 against 19.9; 6 steps 11.1 against 10.8).
+template <bool FC1, int WT, bool SALIGN, bool STAGED>
 struct W4Split : W4Rows<FC1, WT, SALIGN> {
     typedef W4Rows<FC1, WT, SALIGN> B;
     using B::p; using B::lane; using B::wave; using B::r16; using B::q; using B::lo; using B::hi; using B::n;
-    uint32_t coff[WT];
-    u32x4 cw[WT][2];
+    static constexpr int CODES = STAGED ? B::ROWS * 128 : 0;   // LDS bytes of a step's codes
+    uint32_t coff[STAGED ? 2 * WT : WT];
+    u32x4 cw[2 * WT];            // direct: [tile][half]; STAGED: 8 rows each, on their way
+    uint8_t* s_codes;
 
     __device__ __forceinline__ explicit W4Split(const W4Args& a) : B(a, true) {}
 
     __device__ __forceinline__ void load_codes(int k) {
-        const bool live = k * kW4Step + q * 64 < p.Kdim;   // past the row's end: zeros
+        // past the row's end: zeros
+        const bool live = k * kW4Step + (STAGED ? lane % 8 * 32 : q * 64) < p.Kdim;
 #pragma unroll
-        for (int t = 0; t < WT; ++t)
+        for (int i = 0; i < 2 * WT; ++i)
+            cw[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                this->codes, !live ? kOob : k * (kW4Step / 2) + (STAGED ? coff[i] : coff[i / 2] + i % 2 * 16), 0, 0);
+    }
+    __device__ __forceinline__ void store_codes() const {
+        w4_wave_fence();
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                cw[t][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                    this->codes, live ? coff[t] + k * (kW4Step / 2) + h * 16 : kOob, 0, 0);
+        for (int i = 0; i < 2 * WT; ++i) {
+            const int row = 8 * i + lane / 8;
+            *reinterpret_cast<u32x4*>(s_codes + row * 128 + ((lane % 8) ^ (row / 2 % 8)) * 16) = cw[i];
+        }
+        w4_wave_fence();
+    }
+    __device__ __forceinline__ u32x4 operand(int t, int h) const {
+        return STAGED ? *reinterpret_cast<const u32x4*>(
+                            s_codes + (t * 16 + r16) * 128 + ((q * 2 + h) ^ (r16 / 2 % 8)) * 16)
+                      : cw[2 * t + h];
     }
 
     // Routes c0 .. c0 + 16*CT - 1.  fetched: the first step's codes and scales
@@ -292,12 +313,14 @@ struct W4Split : W4Rows<FC1, WT, SALIGN> {
             // every load of the step is issued before the first result is waited for
             __builtin_amdgcn_sched_barrier(0);
             if (k == kp) this->store_scales(k);
+            if (STAGED) store_codes();
 #pragma unroll
             for (int t = 0; t < WT; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) w4_piece<CT>(cw[t][h], this->scale_byte(t, k, kp, h), xw[h], acc[t]);
+                for (int h = 0; h < 2; ++h)
+                    w4_piece<CT>(operand(t, h), this->scale_byte(t, k, kp, h), xw[h], acc[t]);
         }
-        // the parts meet in LDS, in the place of the scale panels
+        // the parts meet in LDS, in the place of codes and scales
         __syncthreads();
         floatx4* mine = s_acc + wave * WT * CT * kWave + lane;
 #pragma unroll
@@ -320,12 +343,12 @@ struct W4Split : W4Rows<FC1, WT, SALIGN> {
 
 // CTMAX: the most 16-route tiles held at once; with 1, a block of more than 16
 // routes reads its weights twice, the second time from the caches.
-template <bool FC1, int WT, int CTMAX, bool SALIGN>
+template <bool FC1, int WT, int CTMAX, bool SALIGN, bool STAGED>
 __global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
-    typedef W4Split<FC1, WT, SALIGN> Wave;
-    constexpr int SCALE_BYTES = kW4Waves * Wave::ROWS * kW4Pitch;
+    typedef W4Split<FC1, WT, SALIGN, STAGED> Wave;
+    constexpr int WAVE_BYTES = Wave::CODES + Wave::ROWS * kW4Pitch;
     constexpr int ACC_BYTES = kW4Waves * WT * CTMAX * kWave * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[SCALE_BYTES > ACC_BYTES ? SCALE_BYTES : ACC_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kW4Waves * WAVE_BYTES > ACC_BYTES ? kW4Waves * WAVE_BYTES : ACC_BYTES];
     static_assert(kW4Waves == kW4Parts, "a part a wave");
     Wave w(p);
     const int b = blockIdx.y;                           // < R / BM
@@ -335,11 +358,14 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
     for (int c = 0; c < 2; ++c) tok[c] = FC1 ? p.sorted_slot_ids[w.slot0 + c * 16 + w.r16] : 0;
     const int e = p.expert_ids[b];                      // device data: range-checked
     if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) return;      // past the extent
-    w.s_scale = smem + w.wave * (Wave::ROWS * kW4Pitch);
+    w.s_codes = smem + w.wave * WAVE_BYTES;
+    w.s_scale = w.s_codes + Wave::CODES;
     w.col0 = blockIdx.x * (16 * Wave::RT);
     w.weights(e);
 #pragma unroll
-    for (int t = 0; t < WT; ++t) w.coff[t] = w.code_offset(t, w.r16, w.q * 32);
+    for (int i = 0; i < (STAGED ? 2 * WT : WT); ++i)
+        w.coff[i] = STAGED ? w.code_offset(i / 2, i % 2 * 8 + w.lane / 8, w.lane % 8 * 16)
+                           : w.code_offset(i, w.r16, w.q * 32);
     if (w.lo < w.hi) {
         w.load_scales(w.lo);
         w.load_codes(w.lo);
@@ -631,7 +657,7 @@ int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
 // tokens of a 512-wide layer 7.6 us instead of 8.4, 64 10.2 against 8.6) and
 // reads at most 24 MB of codes (an expert is read by every token that picks
 // it: 8 tokens of 4 experts of 2048 x 768 22.7 us instead of 23.4, of 8
-// experts 41.5 against 40.5).  One token of the 128-expert layer takes 12.4 us
+// experts 41.5 against 40.5).  One token of the 128-expert layer took 12.4 us
 // instead of 15.7.
 bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {
     return N * H <= 1024 * 16 && N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(24) << 20;
@@ -658,26 +684,29 @@ int check_ptrs(std::initializer_list<const void*> ptrs) {
     return MOE_OK;
 }
 
-template <bool FC1, int CTMAX>
-void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
+template <bool FC1, int WT, int CTMAX, bool SALIGN>
+void launch_split(const W4Args& a, dim3 grid, int steps, hipStream_t s) {
     constexpr int threads = kW4Waves * kWave;
-    const bool salign = a.Kdim % 128 == 0;
-    const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
-    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (salign ? 3 : 2) && steps <= 4;
-    auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
-    if (tiles >= (CTMAX == 1 ? 1200 : 600) && !partial) {
-        const dim3 g = grid((FC1 ? 16 : 32) * kW4Waves);
-        if (salign) w4_stream_kernel<FC1, 2, CTMAX, true><<<g, threads, 0, s>>>(a);
-        else w4_stream_kernel<FC1, 2, CTMAX, false><<<g, threads, 0, s>>>(a);
-    } else if (tiles >= (CTMAX == 1 ? 500 : steps > 2 ? 165 : 400)) {
-        const dim3 g = grid(FC1 ? 32 : 64);
-        if (salign) w4_split_kernel<FC1, 4, CTMAX, true><<<g, threads, 0, s>>>(a);
-        else w4_split_kernel<FC1, 4, CTMAX, false><<<g, threads, 0, s>>>(a);
-    } else {
-        const dim3 g = grid(FC1 ? 16 : 32);
-        if (salign) w4_split_kernel<FC1, 2, CTMAX, true><<<g, threads, 0, s>>>(a);
-        else w4_split_kernel<FC1, 2, CTMAX, false><<<g, threads, 0, s>>>(a);
+    if constexpr (CTMAX == 1) {
+        if (steps >= 2 * kW4Parts) {
+            w4_split_kernel<FC1, WT, CTMAX, SALIGN, true><<<grid, threads, 0, s>>>(a);
+            return;
+        }
     }
+    w4_split_kernel<FC1, WT, CTMAX, SALIGN, false><<<grid, threads, 0, s>>>(a);
+}
+
+template <bool FC1, int CTMAX, bool SALIGN>
+void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
+    const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
+    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (SALIGN ? 3 : 2) && steps <= 4;
+    auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
+    if (tiles >= (CTMAX == 1 ? 1200 : 600) && !partial)
+        w4_stream_kernel<FC1, 2, CTMAX, SALIGN><<<grid((FC1 ? 16 : 32) * kW4Waves), kW4Waves * kWave, 0, s>>>(a);
+    else if (tiles >= (CTMAX == 1 ? 500 : steps > 2 ? 165 : 400))
+        launch_split<FC1, 4, CTMAX, SALIGN>(a, grid(FC1 ? 32 : 64), steps, s);
+    else
+        launch_split<FC1, 2, CTMAX, SALIGN>(a, grid(FC1 ? 16 : 32), steps, s);
 }
 
 // Which kernel: by the most tiles of 64 weight rows that the route list can
@@ -702,8 +731,9 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
 template <bool FC1>
 void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
     const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64));
-    if (mean > 10) launch_w4<FC1, 2>(a, blocks, tiles, s);
-    else launch_w4<FC1, 1>(a, blocks, tiles, s);
+    const bool salign = a.Kdim % 128 == 0;              // rows of scales are whole words
+    if (mean > 10) salign ? launch_w4<FC1, 2, true>(a, blocks, tiles, s) : launch_w4<FC1, 2, false>(a, blocks, tiles, s);
+    else salign ? launch_w4<FC1, 1, true>(a, blocks, tiles, s) : launch_w4<FC1, 1, false>(a, blocks, tiles, s);
 }
 
 int ffn_w4(int which, const uint16_t* x, const uint8_t* w1_codes, const uint8_t* w1_scales,

@@ -137,6 +137,8 @@ SHAPES = {
     "many_tokens_of_a_small_layer": (257, 64, 64, 12, 1),
     "tokens_at_the_bound": (256, 64, 64, 12, 1),
     "split_64_rows_many_rows": (60, 832, 640, 4, 3),
+    "split_64_rows_long": (12, 2176, 1024, 20, 4),
+    "split_64_rows_long_odd": (12, 2112, 1024, 20, 4),
     "stream_early_many_rows": (120, 768, 1280, 12, 3),
     "stream_early_few_rows": (42, 512, 1216, 32, 6),
     "split_steps_end_inside": (64, 1088, 576, 64, 6),
