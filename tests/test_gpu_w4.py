@@ -182,6 +182,19 @@ def test_every_route_to_one_expert_and_none_to_the_others():
     check(buf, x, w1, w2, buf.act, buf.route_out, y)
 
 
+@pytest.mark.parametrize("H,I", [(192, 128), (2112, 192), (192, 2112), (2304, 64), (256, 2304)])
+def test_more_rows_than_the_average_promises(H, I):
+    # 24 rows for each of two experts, 3 an expert on average: the kernels made
+    # for 16 rows go over the weights twice (straight, staged and streaming)
+    N, E, K = 24, 16, 2
+    logits = torch.zeros((N, E), device=DEV)
+    logits[:, 3], logits[:, 11] = 2.0, 1.0
+    buf, x, w1, w2 = case(N, H, I, E, K, logits=logits)
+    assert max(host(buf.route_counts)) == N
+    y = run(buf, x, w1, w2)
+    check(buf, x, w1, w2, buf.act, buf.route_out, y)
+
+
 @pytest.mark.parametrize("H,I,E,K", [(1088, 448, 8, 3), (256, 2048, 4, 4), (1088, 832, 48, 8), (2304, 1280, 64, 2)])
 def test_a_token_alone_equals_the_token_in_any_batch(H, I, E, K):
     N = 260                                   # up to 260 rows an expert
