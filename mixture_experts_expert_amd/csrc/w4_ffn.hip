@@ -392,27 +392,39 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
 // since neighbouring lanes are different rows; that, not memory, bounded them
 // (the address units 60% busy).  Here codes come in whole lines, 8 rows of 128
 // bytes a load, and the routes' rows once for the four waves; both pass
-// through LDS into operand layout (16-byte pieces, swizzled by row: no bank
-// conflicts), and the next step's loads run beside this step's products.
-// 128 tokens of the 128-expert layer: FC1 44 us (52 straight to registers),
-// FC2 26 us (32).  Two steps' loads on their way, 64-row waves, eight waves a
-// workgroup and several column tiles a workgroup in turn were no faster.
+// through LDS into operand layout, and the next step's loads run beside this
+// step's products.  An operand is read from LDS where it is used and one wave
+// needs few registers, which is what lets four workgroups share a compute unit
+// (three with two route tiles).  128 tokens of the 128-expert layer: FC1 44 us
+// (52 straight to registers), FC2 26 us (32); 256 tokens 48 and 30.  Two steps'
+// loads on their way, 64-row waves, waves two by two, eight waves a workgroup
+// and several column tiles a workgroup in turn were no faster.
 template <bool FC1, int WT, bool SALIGN>
 struct W4Stream : W4Rows<FC1, WT, SALIGN> {
     typedef W4Rows<FC1, WT, SALIGN> B;
     using B::p; using B::lane; using B::wave; using B::r16; using B::q; using B::steps; using B::n;
-    uint32_t coff[2 * WT];
+    static_assert(64 % (16 * B::RT) == 0, "a wave's columns are all there or none");
+    // LDS pitches: 16 bytes past the 128 of a row's codes and the 512 of a route's
+    // step, so that 16 lanes with a row each meet no bank twice, and every
+    // operand is one address and a constant away
+    static constexpr int CPITCH = 144, RPITCH = 528;
+    uint32_t coff;               // of the lane's piece of the first 8 rows
     u32x4 cr[2 * WT];            // codes on their way
     uint8_t* s_codes;            // the wave's own
     uint8_t* s_rows;             // the workgroup's
 
     __device__ __forceinline__ explicit W4Stream(const W4Args& a) : B(a, false) {}
 
+    // Load i brings rows 8(i % 2) .. +7 of tile i / 2: this far below the first.
+    __device__ __forceinline__ int below(int i) const {
+        return (FC1 ? i / 4 : i / 2) * 16 + i % 2 * 8 + (FC1 && (i & 2) ? p.ncols : 0);
+    }
     __device__ __forceinline__ void load_codes(int k) {
         const bool live = k * kW4Step + lane % 8 * 32 < p.Kdim;   // past the row's end: zeros
 #pragma unroll
         for (int i = 0; i < 2 * WT; ++i)
-            cr[i] = __builtin_amdgcn_raw_buffer_load_b128(this->codes, live ? coff[i] + k * (kW4Step / 2) : kOob, 0, 0);
+            cr[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                this->codes, live ? coff : kOob, below(i) * (p.Kdim / 2) + k * (kW4Step / 2), 0);
     }
 
     template <int CT>
@@ -434,7 +446,7 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     xr[c][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                        this->rows, live ? aoff[c][j] + k * (kW4Step * 2) : kOob, 0, 0);
+                        this->rows, live ? aoff[c][j] : kOob, k * (kW4Step * 2), 0);
         };
         floatx4 acc[WT][CT], tot[WT][CT];
 #pragma unroll
@@ -446,7 +458,8 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
             load_codes(0);
         }
         load_rows(0);
-        for (int k = 0, kp = 0, part = 0; k < steps; ++k) {
+        int k = 0, kp = 0;
+        auto step = [&]() {
             if (k - kp == kW4Panel) kp = k;
             __builtin_amdgcn_sched_barrier(0);
             if (k > 0) __syncthreads();                 // the last step's rows are read
@@ -454,14 +467,14 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
 #pragma unroll
             for (int i = 0; i < 2 * WT; ++i) {
                 const int row = 8 * i + lane / 8;
-                *reinterpret_cast<u32x4*>(s_codes + row * 128 + ((lane % 8) ^ (row / 2 % 8)) * 16) = cr[i];
+                *reinterpret_cast<u32x4*>(s_codes + row * CPITCH + lane % 8 * 16) = cr[i];
             }
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int row = 4 * wave + 2 * j + lane / 32;
-                    *reinterpret_cast<u32x4*>(s_rows + c * 8192 + row * 512 + ((lane % 32) ^ row) * 16) = xr[c][j];
+                    *reinterpret_cast<u32x4*>(s_rows + (c * 16 + row) * RPITCH + lane % 32 * 16) = xr[c][j];
                 }
             __builtin_amdgcn_sched_barrier(0);
             if (k + 1 < steps) {
@@ -471,50 +484,61 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
             }
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();                            // the rows are there
-            // past a part's last step: its sums join the total
-            while (part < kW4Parts - 1 && k >= w4_part(steps, part + 1)) {
-                ++part;
-#pragma unroll
-                for (int t = 0; t < WT; ++t)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        tot[t][c] += acc[t][c];
-                        acc[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-                    }
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {               // half a step at a time: its operands in registers
-                u32x4 xw[CT][4];
-#pragma unroll
-                for (int c = 0; c < CT; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        xw[c][i] = *reinterpret_cast<const u32x4*>(
-                            s_rows + c * 8192 + r16 * 512 + ((q * 8 + h * 4 + i) ^ r16) * 16);
+                u32x4 cw[WT];
+                float sc[WT];
 #pragma unroll
                 for (int t = 0; t < WT; ++t) {
-                    const u32x4 cw = *reinterpret_cast<const u32x4*>(
-                        s_codes + (t * 16 + r16) * 128 + ((q * 2 + h) ^ (r16 / 2 % 8)) * 16);
-                    w4_piece<CT>(cw, this->scale_byte(t, k, kp, h), xw, acc[t]);
+                    cw[t] = *reinterpret_cast<const u32x4*>(s_codes + (t * 16 + r16) * CPITCH + (q * 2 + h) * 16);
+                    sc[t] = __uint_as_float(this->scale_byte(t, k, kp, h) << 23);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u32x4 xw[CT];
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        xw[c] = *reinterpret_cast<const u32x4*>(
+                            s_rows + (c * 16 + r16) * RPITCH + (q * 8 + h * 4 + i) * 16);
+#pragma unroll
+                    for (int t = 0; t < WT; ++t) {
+                        const bf16x8 a = w4_values(cw[t][i], sc[t]);
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+                            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                a, __builtin_bit_cast(bf16x8, xw[c]), acc[t][c], 0, 0, 0);
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+        };
+#pragma unroll 1
+        for (int part = 0; part < kW4Parts; ++part) {
+#pragma unroll 1
+            for (const int end = w4_part(steps, part + 1); k < end; ++k) step();
+#pragma unroll
+            for (int t = 0; t < WT; ++t)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    tot[t][c] += acc[t][c];
+                    acc[t][c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+                }
         }
 #pragma unroll
         for (int t = 0; t < B::RT; ++t)
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                this->put(t, c0 + 16 * c + r16, [&](int i) { return tot[i][c] + acc[i][c]; });
+                this->put(t, c0 + 16 * c + r16, [&](int i) { return tot[i][c]; });
     }
 };
 
-// With one route tile the registers of four waves a SIMD do (16 tokens: FC1 30 us
-// against 33 with the three that the compiler takes unasked); with two they
-// would spill.
+// Four waves a SIMD with one route tile (16 tokens: FC1 30 us against 33 with
+// three), three with two (256 tokens of 8 experts of 4096 x 1792: FC1 36.5 us
+// against 42.4 with two).
 template <bool FC1, int WT, int CTMAX, bool SALIGN>
-__global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 1) void w4_stream_kernel(W4Args p) {
+__global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 3) void w4_stream_kernel(W4Args p) {
     typedef W4Stream<FC1, WT, SALIGN> Wave;
-    constexpr int SCALE = Wave::ROWS * kW4Pitch, CODES = Wave::ROWS * 128, ROWS = CTMAX * 8192;
+    constexpr int SCALE = Wave::ROWS * kW4Pitch, CODES = Wave::ROWS * Wave::CPITCH, ROWS = CTMAX * 16 * Wave::RPITCH;
     __shared__ __attribute__((aligned(256))) uint8_t smem[ROWS + kW4Waves * (CODES + SCALE)];
     Wave w(p);
     const int b = blockIdx.y;                           // < R / BM
@@ -532,8 +556,7 @@ __global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 1) void w4_strea
     w.s_scale = smem + ROWS + kW4Waves * CODES + w.wave * SCALE;
     w.col0 = (blockIdx.x * kW4Waves + w.wave) * (16 * Wave::RT);
     w.weights(e);
-#pragma unroll
-    for (int i = 0; i < 2 * WT; ++i) w.coff[i] = w.code_offset(i / 2, i % 2 * 8 + w.lane / 8, w.lane % 8 * 16);
+    w.coff = w.code_offset(0, w.lane / 8, w.lane % 8 * 16);
     w.load_scales(0);
     w.load_codes(0);
     __builtin_amdgcn_sched_barrier(0);
@@ -697,11 +720,12 @@ void launch_split(const W4Args& a, dim3 grid, int steps, hipStream_t s) {
 }
 
 template <bool FC1, int CTMAX, bool SALIGN>
-void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
+void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStream_t s) {
     const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
     const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (SALIGN ? 3 : 2) && steps <= 4;
     auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
-    if (tiles >= (CTMAX == 1 ? 1200 : 600) && !partial)
+    const bool early = mean > 4 && steps >= 2 * kW4Parts;
+    if (tiles >= (CTMAX == 2 ? 560 : early ? 800 : 1200) && !partial)
         w4_stream_kernel<FC1, 2, CTMAX, SALIGN><<<grid((FC1 ? 16 : 32) * kW4Waves), kW4Waves * kWave, 0, s>>>(a);
     else if (tiles >= (CTMAX == 1 ? 500 : steps > 2 ? 165 : 400))
         launch_split<FC1, 4, CTMAX, SALIGN>(a, grid(FC1 ? 32 : 64), steps, s);
@@ -714,26 +738,29 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, hipStream_t s) {
 //   * Under 500 (two workgroups a compute unit) the split kernel takes 32-row
 //     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows,
 //     498 3.9 with either, 638 4.9 against 4.0), and from 1200 on the streaming
-//     one fills the device (920 tiles of 2 steps 7.1 us against 5.9 split, 1140
-//     of 12 steps 22.2 against 26.7, 1219 of one 4.9 against 5.7).
+//     one fills the device (920 tiles of 2 steps 6.7 us against 5.9 split, 1219
+//     of one 4.8 against 5.7).  With some rows an expert and long contractions
+//     it does so earlier (4 rows on average, 780 tiles of 8 steps 13.3 us against
+//     15.6, 1140 of 12 21.4 against 26.4; 1.7 rows, 1440 of 18 41.7 against 37.3).
 //   * The streaming kernel pays for a step that the contraction ends inside of:
 //     with 2 to 4 steps split stays ahead (3404 tiles of 576 columns 14.6 us
 //     against 17.3, of 768 18.9 against 17.2).
-//   * Two 16-route tiles are held at once where experts have more than 10 routes
-//     on average (12 a head: 87 us against 92; 8: 80 against 76, the registers of
-//     the second tile cost a workgroup a compute unit).  The split kernel then
+//   * Two 16-route tiles are held at once where experts have more than 8 routes on
+//     average (10 a head: FC1 46 us against 52, FC2 28 against 29; 8: 44.5 against
+//     45.8 and 27.3 against 26.6; 3, of 28 steps: 178 against 170: the second
+//     tile's registers cost a workgroup a compute unit).  The split kernel then
 //     reads twice the operands, and its address units are the time: 64-row
 //     workgroups as soon as 32-row ones are more than one a compute unit (168
 //     tiles of 22 steps 19.5 us against 27.4, 138 of 16 steps 16.1 against 14.5;
 //     with one or two steps later, 300 tiles 4.6 us against 4.5), streaming from
-//     600 (595 of 2 steps 5.6 us against 4.9 split, 663 of one 5.8 against 7.7,
-//     2204 of 5 23 against 32).
+//     560 (576 of 2 steps 8.0 us against 8.7 split, 432 4.9 against 4.0, 2204 of 5
+//     23 against 32).
 template <bool FC1>
 void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
     const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64));
     const bool salign = a.Kdim % 128 == 0;              // rows of scales are whole words
-    if (mean > 10) salign ? launch_w4<FC1, 2, true>(a, blocks, tiles, s) : launch_w4<FC1, 2, false>(a, blocks, tiles, s);
-    else salign ? launch_w4<FC1, 1, true>(a, blocks, tiles, s) : launch_w4<FC1, 1, false>(a, blocks, tiles, s);
+    if (mean > 8) salign ? launch_w4<FC1, 2, true>(a, blocks, tiles, mean, s) : launch_w4<FC1, 2, false>(a, blocks, tiles, mean, s);
+    else salign ? launch_w4<FC1, 1, true>(a, blocks, tiles, mean, s) : launch_w4<FC1, 1, false>(a, blocks, tiles, mean, s);
 }
 
 int ffn_w4(int which, const uint16_t* x, const uint8_t* w1_codes, const uint8_t* w1_scales,
