@@ -699,6 +699,13 @@ def _at(t, dtype, numel: int, name: str, dev: int) -> int:
 
 def _pieces(wide, name: str, per_byte: int, codes, scales):
     """Rows and columns of a block-scaled tensor, from its bf16 form."""
+    try:                                      # two dimensions, the common case
+        rows, cols = wide.shape
+        if (codes.shape == (rows, cols // per_byte) and scales.shape == (rows, cols // 32)
+                and cols > 0 and not cols % 32):
+            return rows, cols
+    except (AttributeError, ValueError):
+        pass
     for t, what in ((wide, name), (codes, "codes"), (scales, "scales")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{what} must be a torch.Tensor")
