@@ -403,3 +403,49 @@ def test_train_in_8_bits_then_serve_in_4():
         o = oracle.dropless_forward(host(T["logits"][:n]), host(T["x"][:n]), v1, v2, w.K)
         assert_bf16_close(host(y), o["y"], f"y of {n} tokens on 4-bit weights")
     assert lad.counts["eager"] < 4
+
+
+@pytest.mark.parametrize("kind", ["q8", "w4"])
+def test_conversions_past_32_bit_offsets(kind):
+    # 2^31 + 2^27 elements: the last rows as in a call of their own
+    rows, cols, tail = 69632, 32768, 40
+    per, dt = (1, torch.int8) if kind == "q8" else (2, torch.uint8)
+    quantize = moe_q8_quantize if kind == "q8" else moe_w4_quantize
+    dequantize = moe_q8_dequantize if kind == "q8" else moe_w4_dequantize
+    v = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    v[-tail:] = torch.randn(tail, cols, generator=g, device=DEV).to(torch.bfloat16)
+    codes = torch.ones(rows, cols // per, dtype=dt, device=DEV)
+    scales = torch.zeros(rows, cols // 32, dtype=torch.uint8, device=DEV)
+    quantize(v, codes, scales)
+    c1, s1 = torch.empty_like(codes[-tail:]), torch.empty_like(scales[-tail:])
+    quantize(v[-tail:], c1, s1)
+    assert torch.equal(codes[-tail:], c1) and torch.equal(scales[-tail:], s1)
+    assert not codes[:-tail].any() and bool((scales[:-tail] == 1).all())
+    back = torch.ones_like(v)
+    dequantize(codes, scales, back)
+    b1 = torch.empty_like(back[-tail:])
+    dequantize(c1, s1, b1)
+    assert torch.equal(back[-tail:], b1) and not back[:-tail].any()
+
+
+def test_swiglu_bwd_q8_past_32_bit_offsets():
+    R, I, tail = 139264, 8192, 24              # 2I codes a row: 2^31 + 2^27 of them
+    g = torch.Generator(device=DEV).manual_seed(6)
+    codes = torch.zeros(R, 2 * I, dtype=torch.int8, device=DEV)
+    scales = torch.full((R, 2 * I // 32), 120, dtype=torch.uint8, device=DEV)
+    d_act = torch.zeros(R, I, dtype=torch.bfloat16, device=DEV)
+    probs = torch.rand(R, generator=g, device=DEV)
+    codes[-tail:] = torch.randint(-127, 128, (tail, 2 * I), generator=g, device=DEV, dtype=torch.int8)
+    d_act[-tail:] = torch.randn(tail, I, generator=g, device=DEV).to(torch.bfloat16)
+
+    def run(c, s, d, p):
+        n = d.shape[0]
+        out = [torch.ones(n, I, dtype=torch.bfloat16, device=DEV), torch.ones(n, 2 * I, dtype=torch.bfloat16, device=DEV),
+               torch.ones(n, device=DEV)]
+        moe_swiglu_bwd_q8(c, s, d, p, *out)
+        return out
+    whole = run(codes, scales, d_act, probs)
+    last = run(codes[-tail:], scales[-tail:], d_act[-tail:], probs[-tail:].clone())
+    for a, b in zip(whole, last):
+        assert torch.equal(a[-tail:], b) and not a[:-tail].any()

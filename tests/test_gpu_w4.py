@@ -355,3 +355,24 @@ def test_serving_ladder_on_4_bit_weights():
             o = oracle.dropless_forward(host(lg[:n]), host(x[:n]), v1, v2, w.K)
             assert_bf16_close(host(y), o["y"], f"y (n={n}) vs oracle")
     assert sum(v for k, v in lad.counts.items() if k != "eager") >= 6
+
+
+def test_weights_past_32_bit_offsets():
+    # codes of 80 experts are over 2^31 bytes; the last expert as in a layer of its own
+    N, H, I, E = 5, 7168, 4096, 80
+    g = torch.Generator(device=DEV).manual_seed(9)
+
+    def big(rows, cols):
+        w = W4Weights(torch.zeros(E, rows, cols // 2, dtype=torch.uint8, device=DEV),
+                      torch.full((E, rows, cols // 32), 119, dtype=torch.uint8, device=DEV))
+        w.codes[-1] = torch.randint(0, 256, (rows, cols // 2), generator=g, device=DEV, dtype=torch.uint8)
+        return w
+    w1, w2 = big(2 * I, H), big(H, I)
+    assert w1.codes.numel() > 2 ** 31
+    x = torch.randn(N, H, generator=g, device=DEV).to(torch.bfloat16)
+    logits = torch.zeros((N, E), device=DEV)
+    logits[:, -1] = 100.0                      # a probability of 1
+    got = forward_dropless(DroplessBuffers(N, H, I, E, 1, DEV, w4=True), logits, x, w1, w2)
+    one = [W4Weights(w.codes[-1:], w.scales[-1:]) for w in (w1, w2)]
+    alone = forward_dropless(DroplessBuffers(N, H, I, 1, 1, DEV, w4=True), logits[:, -1:].contiguous(), x, *one)
+    assert torch.equal(got, alone) and bool((got != 0).any())
