@@ -4,6 +4,8 @@
 // All are HBM-bound passes: every input is read once and every output written
 // once, 8 columns a lane (16 bytes of bf16), so a group of 32 columns is four
 // neighbouring lanes, which share its largest magnitude in two lane swaps.
+// 8192 rows of 7168: 32 us each way, 5.5 TB/s, what a plain copy reaches (two
+// pieces a lane the same, four 33 and 35 us).
 #include <algorithm>
 #include <initializer_list>
 

@@ -234,6 +234,23 @@ def test_nan_infinity_and_garbage_stay_where_they_belong():
     assert torch.equal(y[:, cols], clean[:, cols])
 
 
+@pytest.mark.parametrize("name", ["stream_early_few_rows", "stream_early_many_rows", "split_64_rows_long_odd", "odd_steps"])
+def test_every_kernel_leaves_pads_and_other_tokens_alone(name):
+    buf, x, w1, w2 = case(*SHAPES[name])
+    clean = run(buf, x, w1, w2).clone()
+    buf.act.fill_(5.0)
+    buf.route_out.fill_(5.0)
+    x2 = x.clone()
+    x2[2, 1::7] = float("nan")
+    y = run(buf, x2, w1, w2)
+    keep = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    keep[2] = False
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[2]).all())
+    pads = torch.ones(buf.R, dtype=torch.bool, device=DEV)
+    pads[torch.from_numpy(live_slots(buf)[0]).to(DEV)] = False
+    assert bool((buf.act[pads] == 5).all()) and bool((buf.route_out[pads] == 5).all())
+
+
 def test_list_entries_out_of_range_are_dropped():
     """Device data is range-checked: experts, blocks, counts and tokens that
     name nothing read and write nothing (codes past the routes stay as set)."""
