@@ -240,7 +240,13 @@ extern "C" int moe_swiglu_bwd_q8(const int8_t* codes, const uint8_t* scales, con
         if (!aligned16(q)) return MOE_ERR_MISALIGNED;
     }
     const int per = std::max(1, kBwdThreads / (I / 8));
-    swiglu_bwd_q8_kernel<<<static_cast<unsigned>((R + per - 1) / per), kBwdThreads, 0, stream>>>(
-        codes, scales, d_act, slot_probs, static_cast<int>(R), I, per, act, d_preact, d_prob);
+    // a grid of 2^32 threads or more wraps without an error: at most 2^23 workgroups a launch
+    const int64_t most = static_cast<int64_t>(per) << 23;
+    for (int64_t r = 0; r < R; r += most) {
+        const int n = static_cast<int>(std::min(most, R - r));
+        swiglu_bwd_q8_kernel<<<static_cast<unsigned>((n + per - 1) / per), kBwdThreads, 0, stream>>>(
+            codes + r * 2 * I, scales + r * (2 * I / kGroup), d_act + r * I, slot_probs + r, n, I, per,
+            act + r * I, d_preact + r * 2 * I, d_prob + r);
+    }
     return launch_status();
 }
