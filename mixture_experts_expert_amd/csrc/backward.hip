@@ -11,6 +11,8 @@
 //
 // Both kernels are HBM-bound elementwise passes; they read each input once
 // with 16-byte loads and write each output once.
+#include <algorithm>
+
 #include "gemm_common.h"
 
 namespace moe {
@@ -113,9 +115,14 @@ extern "C" int moe_swiglu_bwd(const uint16_t* preact, const uint16_t* d_act,
         if (!q) return MOE_ERR_INVALID_ARG;
         if (!aligned16(q)) return MOE_ERR_MISALIGNED;
     }
-    const int64_t blocks = (R + 3) / 4;
-    swiglu_bwd_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        preact, d_act, slot_probs, static_cast<int>(R), I, act, d_preact, d_prob);
+    // a grid of 2^32 threads or more wraps without an error: at most 2^23 workgroups a launch
+    const int64_t most = static_cast<int64_t>(4) << 23;
+    for (int64_t r = 0; r < R; r += most) {
+        const int n = static_cast<int>(std::min(most, R - r));
+        swiglu_bwd_kernel<<<static_cast<unsigned>((n + 3) / 4), 256, 0, stream>>>(
+            preact + r * 2 * I, d_act + r * I, slot_probs + r, n, I, act + r * I, d_preact + r * 2 * I,
+            d_prob + r);
+    }
     return launch_status();
 }
 
