@@ -10,6 +10,8 @@
 // row's threads), issues all K row loads before summing, adds them in float32
 // in k order starting from +0.0, and stores 16 bytes of y.  HBM-bound: the
 // route rows are read once, y is written once.
+#include <algorithm>
+
 #include "moe_common.h"
 
 namespace moe {
@@ -111,10 +113,14 @@ extern "C" int moe_dispatch_rows(const uint16_t* x, const int32_t* sorted_slot_i
     if (R == 0) return MOE_OK;
     if (!x || !sorted_slot_ids || !rows) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(sorted_slot_ids) || !aligned16(rows)) return MOE_ERR_MISALIGNED;
-    const int64_t items = R * (H / 8);
-    const int64_t blocks = (items + 255) / 256;
-    if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-    dispatch_rows_kernel<<<static_cast<int>(blocks), 256, 0, stream>>>(
-        x, sorted_slot_ids, static_cast<int>(N), H, static_cast<int>(R), rows);
+    if ((R * (H / 8) + 255) / 256 > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // a grid of 2^32 threads or more wraps without an error: at most 2^31 a launch
+    const int64_t most = (static_cast<int64_t>(1) << 31) / (H / 8);
+    for (int64_t r = 0; r < R; r += most) {
+        const int n = static_cast<int>(std::min(most, R - r));
+        const int64_t items = static_cast<int64_t>(n) * (H / 8);
+        dispatch_rows_kernel<<<static_cast<int>((items + 255) / 256), 256, 0, stream>>>(
+            x, sorted_slot_ids + r, static_cast<int>(N), H, n, rows + r * H);
+    }
     return launch_status();
 }
