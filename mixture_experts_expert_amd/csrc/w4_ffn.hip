@@ -722,12 +722,13 @@ void launch_split(const W4Args& a, dim3 grid, int steps, hipStream_t s) {
 template <bool FC1, int CTMAX, bool SALIGN>
 void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStream_t s) {
     const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
-    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (SALIGN ? 3 : 2) && steps <= 4;
+    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (SALIGN ? 3 : 2) && steps <= 4 &&
+                         tiles < (FC1 ? 2000 : SALIGN ? 6000 : INT64_MAX);
     auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
     const bool early = mean > 4 && steps >= 2 * kW4Parts;
     if (tiles >= (CTMAX == 2 ? 560 : early ? 800 : 1200) && !partial)
         w4_stream_kernel<FC1, 2, CTMAX, SALIGN><<<grid((FC1 ? 16 : 32) * kW4Waves), kW4Waves * kWave, 0, s>>>(a);
-    else if (tiles >= (CTMAX == 1 ? 500 : steps > 2 ? 165 : 400))
+    else if (tiles >= (CTMAX == 1 ? (mean > 2 ? 500 : 640) : steps > 2 ? 165 : 400))
         launch_split<FC1, 4, CTMAX, SALIGN>(a, grid(FC1 ? 32 : 64), steps, s);
     else
         launch_split<FC1, 2, CTMAX, SALIGN>(a, grid(FC1 ? 16 : 32), steps, s);
@@ -736,15 +737,24 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStrea
 // Which kernel: by the most tiles of 64 weight rows that the route list can
 // ask for.
 //   * Under 500 (two workgroups a compute unit) the split kernel takes 32-row
-//     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows,
-//     498 3.9 with either, 638 4.9 against 4.0), and from 1200 on the streaming
-//     one fills the device (920 tiles of 2 steps 6.7 us against 5.9 split, 1219
-//     of one 4.8 against 5.7).  With some rows an expert and long contractions
-//     it does so earlier (4 rows on average, 780 tiles of 8 steps 13.3 us against
-//     15.6, 1140 of 12 21.4 against 26.4; 1.7 rows, 1440 of 18 41.7 against 37.3).
-//   * The streaming kernel pays for a step that the contraction ends inside of:
-//     with 2 to 4 steps split stays ahead (3404 tiles of 576 columns 14.6 us
-//     against 17.3, of 768 18.9 against 17.2).
+//     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows;
+//     with 4 rows an expert on average 490 of 4 steps 7.4 with either, 560 of 8
+//     10.4 against 9.8), under 640 where experts have one or two rows (one row,
+//     512 of 8 steps 7.5 us against 8.5, 640 8.9 against 9.0, 1024 of 3 7.2
+//     against 6.5).  From 1200 on the streaming kernel fills the device (920
+//     tiles of 2 steps 6.7 us against 5.9 split, 1219 of one 4.8 against 5.7).
+//     With some rows an expert and long contractions it does so earlier (4 rows
+//     on average, 780 tiles of 8 steps 13.3 us against 15.6, 1140 of 12 21.4
+//     against 26.4; 1.7 rows, 1440 of 18 41.7 against 37.3).
+//   * The streaming kernel pays for a step that the contraction ends inside of,
+//     which counts with 2 to 4 steps and few rounds of workgroups.  FC1: 1260
+//     tiles of 576 columns 10.0 us against 9.5 split, 2240 12.6 against 13.0, 8960
+//     39 against 47, of 640 40 against 52.  FC2, whose float32 rows split writes
+//     sooner: 2240 tiles of 640 columns 12.8 against 12.1, 4480 20.9 against 21.2,
+//     6160 29.7 against 30.8, 8960 40 against 43; where rows of scales are not
+//     whole words split stays ahead with one row an expert (8192 of 832 35 against
+//     31) and with 4 (8960 52.8 against 49.8), and with 8 is 3% behind (9984 58.0
+//     against 56.5).
 //   * Two 16-route tiles are held at once where experts have more than 8 routes on
 //     average (10 a head: FC1 46 us against 52, FC2 28 against 29; 8: 44.5 against
 //     45.8 and 27.3 against 26.6; 3, of 28 steps: 178 against 170: the second

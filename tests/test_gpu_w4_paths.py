@@ -64,6 +64,18 @@ SHAPES = {
     "fc1_64_rows": (12, 1024, 1024, 20, 4),
     "fc2_64_rows_long_odd": (12, 1664, 2112, 20, 4),
     "fc2_streams_two_route_tiles": (64, 3264, 256, 8, 2),
+    # steps that the contraction ends inside of: split for few tiles, streaming
+    # for many, in FC1 and in FC2 with whole words of scales
+    "fc1_ends_inside_split": (64, 576, 576, 64, 4),
+    "fc1_ends_inside_streams": (64, 576, 960, 64, 4),
+    "fc1_ends_inside_streams_aligned": (64, 640, 960, 64, 4),
+    "fc1_ends_inside_streams_few_rows": (16, 832, 1088, 64, 4),
+    "fc2_ends_inside_split": (64, 5376, 640, 64, 4),
+    "fc2_ends_inside_streams": (64, 5632, 640, 64, 4),
+    "fc2_ends_inside_split_odd": (64, 5632, 576, 64, 4),
+    # workgroups of 32 or 64 rows with one row an expert
+    "split_32_rows_few_rows": (8, 512, 576, 32, 4),
+    "split_64_rows_few_rows": (8, 512, 640, 32, 4),
     "twelve_routes_a_token": (33, 256, 128, 24, 12),
     "nine_routes_a_token": (5, 192, 64, 9, 9),
     "sixteen_routes_a_token": (70, 64, 192, 40, 16),
@@ -79,7 +91,7 @@ def test_form(name):
     buf.route_out.fill_(7.0)
     y = run(buf, x, w1, w2).clone()
     assert pads_as_set(buf)
-    check(buf, x, w1, w2, buf.act, buf.route_out, y)
+    check(buf, x, w1, w2, buf.act, buf.route_out, y, experts=[0, 3, SHAPES[name][3] - 1] if buf.E > 48 else None)
     N, E = SHAPES[name][0], SHAPES[name][3]
     logits = torch.from_numpy(np.ascontiguousarray(moe_inputs.make_logits(N, E, 1), dtype=np.float32)).to(DEV)
     alone(buf, logits, x, w1, w2, y, (0, N // 2, N - 1))
