@@ -676,14 +676,14 @@ int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
 }
 
 // Whether FC2 and the combine run in one launch, token by token: while that is
-// at most 1024 workgroups (two rounds of 16 waves over the compute units; 32
+// at most four workgroups a compute unit (two rounds of their 16 waves; 1024: 32
 // tokens of a 512-wide layer 7.6 us instead of 8.4, 64 10.2 against 8.6) and
 // reads at most 24 MB of codes (an expert is read by every token that picks
 // it: 8 tokens of 4 experts of 2048 x 768 22.7 us instead of 23.4, of 8
 // experts 41.5 against 40.5).  One token of the 128-expert layer took 12.4 us
 // instead of 15.7.
 bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {
-    return N * H <= 1024 * 16 && N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(24) << 20;
+    return N * H / 16 <= 4 * device_cus() && N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(24) << 20;
 }
 
 int check_w4(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K, int64_t* R) {
@@ -735,7 +735,8 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStrea
 }
 
 // Which kernel: by the most tiles of 64 weight rows that the route list can
-// ask for.
+// ask for, counted as for 256 compute units (all of this device's; a partition
+// of it has fewer).
 //   * Under 500 (two workgroups a compute unit) the split kernel takes 32-row
 //     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows;
 //     with 4 rows an expert on average 490 of 4 steps 7.4 with either, 560 of 8
@@ -767,7 +768,7 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStrea
 //     23 against 32).
 template <bool FC1>
 void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
-    const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64));
+    const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64)) * 256 / device_cus();
     const bool salign = a.Kdim % 128 == 0;              // rows of scales are whole words
     if (mean > 8) salign ? launch_w4<FC1, 2, true>(a, blocks, tiles, mean, s) : launch_w4<FC1, 2, false>(a, blocks, tiles, mean, s);
     else salign ? launch_w4<FC1, 1, true>(a, blocks, tiles, mean, s) : launch_w4<FC1, 1, false>(a, blocks, tiles, mean, s);
