@@ -23,7 +23,10 @@
  *       in the low half;                                    value c * 2^(b-127)
  *
  * (w4 is laid out like the OCP microscaling format MXFP4, so a checkpoint in
- * that format, codes [rows, K/2] and scales [rows, K/32], is used as it is.)
+ * that format, codes [rows, K/2] and scales [rows, K/32], is used as it is:
+ * every byte from 0 to 254 counts exactly, except that the magnitudes that no
+ * float32 or bf16 holds, 2^128 and more (codes 4 and 6 at b = 253, 2 to 6 at
+ * 254), are infinite.)
  * The quantizers pick the smallest b >= 1 with which no element of the group
  * is off by more than half a step of its codes, and round to nearest, ties
  * to the even code; a group of zeros has b = 1 and codes 0.  b = 255 stands
@@ -87,7 +90,7 @@ int moe_q8_dequantize(const int8_t* codes, const uint8_t* scales, int64_t rows, 
  * the other tokens, or on its slot.  Any N of the routing envelope is served;
  * the kernels are made for few routes per expert (up to about 64), where the
  * weights' bytes decide.  With hundreds of rows per expert the bf16 layer is
- * faster.  Groups whose scale is below 2^-100 may count as zero.
+ * faster.
  *
  * H and I multiples of 64 in [64, 16384]; (N + 1)*H*2, (N + BM)*max(H, I)*4
  * and one expert's codes I*H below 2^31. */
