@@ -247,9 +247,12 @@ struct W4Rows {
 // when a wave has one step.  Lane (r16, q) takes the 32 bytes of codes of
 // columns 64q .. 64q+63 of its row, and the other operand's lanes those columns
 // of their rows.  STAGED: the codes come in whole lines and through LDS of the
-// wave's own (which needs no barrier), for contractions of several steps a wave,
-// where 64 cache accesses a load add up (one token, H 2048: FC1 5.6 us against
-// 6.2, H 6912 17.2 against 19.9; 6 steps 11.1 against 10.8).
+// wave's own (which needs no barrier), for contractions of 6 steps and more,
+// where 64 cache accesses a load add up (FC1 of one token in 64 or 128 experts:
+// 6 steps 5.3 us against 5.7, 8 5.9 against 6.5, 27 10.7 against 13.0; FC2 of 8
+// rows an expert, 5 steps 8.8 against 8.6, 6 9.0 against 9.3).  Only where rows are
+// whole words of scales: the codes of the others begin in the middle of a 64-byte
+// piece (9 steps 7.0 us staged, 6.5 straight, 17 9.4 against 9.1).
 template <bool FC1, int WT, bool SALIGN, bool STAGED>
 struct W4Split : W4Rows<FC1, WT, SALIGN> {
     typedef W4Rows<FC1, WT, SALIGN> B;
@@ -710,8 +713,8 @@ int check_ptrs(std::initializer_list<const void*> ptrs) {
 template <bool FC1, int WT, int CTMAX, bool SALIGN>
 void launch_split(const W4Args& a, dim3 grid, int steps, hipStream_t s) {
     constexpr int threads = kW4Waves * kWave;
-    if constexpr (CTMAX == 1) {
-        if (steps >= 2 * kW4Parts) {
+    if constexpr (CTMAX == 1 && SALIGN) {
+        if (steps >= 6) {
             w4_split_kernel<FC1, WT, CTMAX, SALIGN, true><<<grid, threads, 0, s>>>(a);
             return;
         }

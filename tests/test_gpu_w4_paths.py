@@ -76,6 +76,11 @@ SHAPES = {
     # workgroups of 32 or 64 rows with one row an expert
     "split_32_rows_few_rows": (8, 512, 576, 32, 4),
     "split_64_rows_few_rows": (8, 512, 640, 32, 4),
+    # codes straight to registers or through LDS
+    "five_and_six_steps": (4, 1280, 1536, 32, 4),
+    "six_and_five_steps": (4, 1536, 1280, 32, 4),
+    "seven_steps_odd_scales": (4, 1600, 1728, 32, 4),
+    "nine_steps_odd_scales": (9, 2112, 2240, 16, 2),
     "twelve_routes_a_token": (33, 256, 128, 24, 12),
     "nine_routes_a_token": (5, 192, 64, 9, 9),
     "sixteen_routes_a_token": (70, 64, 192, 40, 16),
