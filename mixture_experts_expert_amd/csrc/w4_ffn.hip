@@ -678,15 +678,18 @@ int w4_blocks(int64_t N, int32_t E, int32_t K, int64_t R) {
     return static_cast<int>(std::min<int64_t>(R, routes + (kBlockM - 1) * std::min<int64_t>(E, routes)) / kBlockM);
 }
 
-// Whether FC2 and the combine run in one launch, token by token: while that is
-// at most four workgroups a compute unit (two rounds of their 16 waves; 1024: 32
-// tokens of a 512-wide layer 7.6 us instead of 8.4, 64 10.2 against 8.6) and
-// reads at most 24 MB of codes (an expert is read by every token that picks
-// it: 8 tokens of 4 experts of 2048 x 768 22.7 us instead of 23.4, of 8
-// experts 41.5 against 40.5).  One token of the 128-expert layer took 12.4 us
-// instead of 15.7.
+// Whether FC2 and the combine run in one launch, token by token.  An expert is
+// read by every token that picks it, and a compute unit runs two workgroups of
+// 16 waves at once: it pays while that is at most 24 MB of codes (12 us instead of
+// 15.2 for one token of the 128-expert layer, 6 MB; 4 tokens, 24 MB 21.7 instead
+// of 24.9; one of 64 experts of 7168 x 2048, 56 MB 51.9 against 49.3) and three
+// workgroups a compute unit (768: 24 tokens of a 512-wide layer 8.9 instead of
+// 9.0, 12 of 32 experts of 1024 x 768 16.3 instead of 16.4; 1024: 16 of them 18.0
+// against 16.7, 8 of 8 experts of 2048 x 768 15.8 against 13.7), four where the
+// codes are few (256 tokens of a 64-wide layer 7.6 instead of 8.9).
 bool w4_by_token(int64_t N, int32_t H, int32_t I, int32_t K) {
-    return N * H / 16 <= 4 * device_cus() && N * K * (static_cast<int64_t>(H) * I / 2) <= static_cast<int64_t>(24) << 20;
+    const int64_t codes = N * K * (static_cast<int64_t>(H) * I / 2), mb = 1 << 20;
+    return N * H / 16 <= (codes <= 4 * mb ? 4 : 3) * device_cus() && codes <= 24 * mb;
 }
 
 int check_w4(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K, int64_t* R) {

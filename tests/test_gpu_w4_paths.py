@@ -81,6 +81,9 @@ SHAPES = {
     "six_and_five_steps": (4, 1536, 1280, 32, 4),
     "seven_steps_odd_scales": (4, 1600, 1728, 32, 4),
     "nine_steps_odd_scales": (9, 2112, 2240, 16, 2),
+    # FC2 with the token's sum or without
+    "tokens_in_one_launch": (24, 512, 512, 16, 2),
+    "tokens_in_two_launches": (25, 512, 512, 16, 2),
     "twelve_routes_a_token": (33, 256, 128, 24, 12),
     "nine_routes_a_token": (5, 192, 64, 9, 9),
     "sixteen_routes_a_token": (70, 64, 192, 40, 16),
