@@ -728,13 +728,20 @@ void launch_split(const W4Args& a, dim3 grid, int steps, hipStream_t s) {
 template <bool FC1, int CTMAX, bool SALIGN>
 void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStream_t s) {
     const int steps = (a.Kdim + kW4Step - 1) / kW4Step;
-    const bool partial = CTMAX == 1 && a.Kdim % kW4Step != 0 && steps >= (SALIGN ? 3 : 2) && steps <= 4 &&
-                         tiles < (FC1 ? 2000 : SALIGN ? 6000 : INT64_MAX);
+    const bool inside = a.Kdim % kW4Step != 0, brief = inside && steps >= (SALIGN ? 3 : 2) && steps <= 4;
+    int64_t rows64, stream;      // tiles from which on: 64-row workgroups, the streaming kernel
+    if (CTMAX == 1) {
+        rows64 = mean > 2 ? 500 : 640;
+        stream = brief ? (FC1 ? 2000 : SALIGN ? 6000 : INT64_MAX) : mean > 4 ? 800 : mean > 2 ? 900 : 1100;
+    } else {
+        rows64 = steps > 2 ? 200 : 340;
+        if (brief && !SALIGN) stream = mean > 24 ? 650 : 900;
+        else stream = mean > 48 ? 300 : mean > 24 ? 350 : inside && steps <= 7 ? 650 : 480;
+    }
     auto grid = [&](int cols) { return dim3((a.ncols + cols - 1) / cols, blocks); };
-    const bool early = mean > 4 && steps >= 2 * kW4Parts;
-    if (tiles >= (CTMAX == 2 ? 560 : early ? 800 : 1200) && !partial)
+    if (tiles >= stream)
         w4_stream_kernel<FC1, 2, CTMAX, SALIGN><<<grid((FC1 ? 16 : 32) * kW4Waves), kW4Waves * kWave, 0, s>>>(a);
-    else if (tiles >= (CTMAX == 1 ? (mean > 2 ? 500 : 640) : steps > 2 ? 165 : 400))
+    else if (tiles >= rows64)
         launch_split<FC1, 4, CTMAX, SALIGN>(a, grid(FC1 ? 32 : 64), steps, s);
     else
         launch_split<FC1, 2, CTMAX, SALIGN>(a, grid(FC1 ? 16 : 32), steps, s);
@@ -742,36 +749,41 @@ void launch_w4(const W4Args& a, int blocks, int64_t tiles, double mean, hipStrea
 
 // Which kernel: by the most tiles of 64 weight rows that the route list can
 // ask for, counted as for 256 compute units (all of this device's; a partition
-// of it has fewer).
-//   * Under 500 (two workgroups a compute unit) the split kernel takes 32-row
-//     workgroups, for more of them (264 tiles 4.7 us against 5.0 with 64 rows;
-//     with 4 rows an expert on average 490 of 4 steps 7.4 with either, 560 of 8
-//     10.4 against 9.8), under 640 where experts have one or two rows (one row,
-//     512 of 8 steps 7.5 us against 8.5, 640 8.9 against 9.0, 1024 of 3 7.2
-//     against 6.5).  From 1200 on the streaming kernel fills the device (920
-//     tiles of 2 steps 6.7 us against 5.9 split, 1219 of one 4.8 against 5.7).
-//     With some rows an expert and long contractions it does so earlier (4 rows
-//     on average, 780 tiles of 8 steps 13.3 us against 15.6, 1140 of 12 21.4
-//     against 26.4; 1.7 rows, 1440 of 18 41.7 against 37.3).
-//   * The streaming kernel pays for a step that the contraction ends inside of,
-//     which counts with 2 to 4 steps and few rounds of workgroups.  FC1: 1260
-//     tiles of 576 columns 10.0 us against 9.5 split, 2240 12.6 against 13.0, 8960
-//     39 against 47, of 640 40 against 52.  FC2, whose float32 rows split writes
-//     sooner: 2240 tiles of 640 columns 12.8 against 12.1, 4480 20.9 against 21.2,
-//     6160 29.7 against 30.8, 8960 40 against 43; where rows of scales are not
-//     whole words split stays ahead with one row an expert (8192 of 832 35 against
-//     31) and with 4 (8960 52.8 against 49.8), and with 8 is 3% behind (9984 58.0
-//     against 56.5).
+// of it has fewer), and the routes an expert has on average.  Over 508 sizes
+// about the bounds the choice is 0.9% off the fastest of the three kernels on
+// average, 14% at most.
+//   * Few tiles: the split kernel with 32-row workgroups, for more of them (264
+//     tiles 4.7 us against 5.0 with 64 rows).  With one or two routes an expert up
+//     to 640 (one, 512 tiles of 8 steps 7.5 us against 8.5, 640 8.9 against 9.0,
+//     1024 of 3 7.2 against 6.5), with more, whose operands they read more often,
+//     up to 500 (4, 490 tiles of 4 steps 7.4 with either, 560 of 8 10.4 against
+//     9.8).
+//   * Many: the streaming kernel, which with more routes pays sooner: from 1100
+//     (4 steps, one route: 960 tiles 8.5 us with either, 1216 8.7 against 10.0
+//     split), 900 (4: 770 8.7 against 9.0, 910 8.9 against 11.1; of 28 steps 910
+//     45 against 46, 1190, where its last round is short, 63 against 56) or 800
+//     (8: 624 of 8 steps 10.4 with either, 858 of 4 8.8 against 9.5).
+//   * It pays for a step that the contraction ends inside of, which counts with 2
+//     to 4 steps and few rounds of workgroups.  FC1: 1260 tiles of 576 columns
+//     10.0 us against 9.5 split, 2240 12.6 against 13.0, 8960 39 against 47, of 640
+//     40 against 52.  FC2, whose float32 rows split writes sooner: 2240 tiles of
+//     640 columns 12.8 against 12.1, 4480 20.9 against 21.2, 6160 29.7 against
+//     30.8, 8960 40 against 43; where rows of scales are not whole words split
+//     stays ahead with one route an expert (8192 of 832 35 against 31) and with 4
+//     (8960 52.8 against 49.8), and with 8 is 3% behind (9984 58.0 against 56.5).
 //   * Two 16-route tiles are held at once where experts have more than 8 routes on
-//     average (10 a head: FC1 46 us against 52, FC2 28 against 29; 8: 44.5 against
-//     45.8 and 27.3 against 26.6; 3, of 28 steps: 178 against 170: the second
-//     tile's registers cost a workgroup a compute unit).  The split kernel then
-//     reads twice the operands, and its address units are the time: 64-row
-//     workgroups as soon as 32-row ones are more than one a compute unit (168
-//     tiles of 22 steps 19.5 us against 27.4, 138 of 16 steps 16.1 against 14.5;
-//     with one or two steps later, 300 tiles 4.6 us against 4.5), streaming from
-//     560 (576 of 2 steps 8.0 us against 8.7 split, 432 4.9 against 4.0, 2204 of 5
-//     23 against 32).
+//     average (10: FC1 46 us against 52, FC2 28 against 29; 8: 44.5 against 45.8
+//     and 27.3 against 26.6; 3, of 28 steps: 178 against 170: the second tile's
+//     registers cost a workgroup a compute unit).  The split kernel then reads
+//     twice the operands, and its address units are the time: 64-row workgroups
+//     from 200 tiles (4 steps: 154 6.0 us against 5.0 with 32 rows, 210 6.5 against
+//     7.5), with one or two steps from 340 (286 4.5 against 4.2, 374 4.7 against
+//     5.3).  Streaming from 480 (16 routes, 4 steps: 414 8.8 against 8.3 split, 506
+//     9.0 with either, 782 9.7 against 11.5), 350 (32: 270 8.5 against 7.0, 390 8.9
+//     against 9.7) or 300 (64: 230 8.7 against 7.2, 322 8.9 against 10.1); with 5 to
+//     7 steps that end inside and up to 24 routes 650 (598 10.3 against 9.9, 782
+//     11.5 against 12.1); with 2 to 4 of them and scales that are not whole words
+//     900, with more routes 650 (16: 782 tiles of 576 columns 8.3 against 7.9).
 template <bool FC1>
 void dispatch_w4(const W4Args& a, int blocks, double mean, hipStream_t s) {
     const int64_t tiles = static_cast<int64_t>(blocks) * (a.ncols / (FC1 ? 32 : 64)) * 256 / device_cus();

@@ -103,3 +103,27 @@ def test_form(name):
     N, E = SHAPES[name][0], SHAPES[name][3]
     logits = torch.from_numpy(np.ascontiguousarray(moe_inputs.make_logits(N, E, 1), dtype=np.float32)).to(DEV)
     alone(buf, logits, x, w1, w2, y, (0, N // 2, N - 1))
+
+
+@pytest.mark.parametrize("shape", [
+    # one route tile: 4 routes an expert, 840 and 910 tiles; one, 1088 and 1152
+    (32, 512, 768, 32, 4), (32, 512, 832, 32, 4), (8, 512, 1088, 32, 4), (8, 512, 1152, 32, 4),
+    # two: 32 or 64 weight rows, with 2 steps and with 4
+    (64, 512, 960, 8, 2), (64, 512, 1024, 8, 2), (64, 1024, 576, 8, 2), (64, 1024, 640, 8, 2),
+    # streaming with 16, 32 and 64 routes an expert
+    (64, 512, 1344, 8, 2), (64, 512, 1408, 8, 2), (128, 512, 704, 8, 2), (128, 512, 768, 8, 2),
+    (256, 512, 384, 8, 2), (256, 512, 448, 8, 2),
+    # and where the contraction ends inside a step
+    (64, 1088, 1856, 8, 2), (64, 1088, 1920, 8, 2), (64, 576, 2560, 8, 2), (64, 576, 2624, 8, 2),
+    (128, 576, 1344, 8, 2), (128, 576, 1408, 8, 2), (256, 1152, 448, 8, 2),
+], ids=str)
+def test_either_side_of_the_bounds(shape):
+    say(f"[w4] {shape}")
+    buf, x, w1, w2 = case(*shape)
+    buf.act.fill_(7.0)
+    buf.route_out.fill_(7.0)
+    y = run(buf, x, w1, w2).clone()
+    assert pads_as_set(buf)
+    check(buf, x, w1, w2, buf.act, buf.route_out, y, experts=[0, buf.E - 1])
+    logits = torch.from_numpy(np.ascontiguousarray(moe_inputs.make_logits(buf.N, buf.E, 1), dtype=np.float32)).to(DEV)
+    alone(buf, logits, x, w1, w2, y, (0, buf.N - 1))
