@@ -89,8 +89,11 @@ int moe_q8_dequantize(const int8_t* codes, const uint8_t* scales, int64_t rows, 
  * result depends on its own row and expert alone, bit for bit: not on N, on
  * the other tokens, or on its slot.  Any N of the routing envelope is served;
  * the kernels are made for few routes per expert (up to about 64), where the
- * weights' bytes decide.  With hundreds of rows per expert the bf16 layer is
- * faster.
+ * weights' bytes decide.  An expert's weights are read and converted once for
+ * every 32 of its routes, so with hundreds of them the bf16 layer is faster
+ * (128 experts of 2048 x 768: 64 routes an expert 182 us against 235 in bf16,
+ * 128 314 against 282; 8 of 4096 x 1792: 256 158 against 209, 512 282 against
+ * 271; 64 of 7168 x 2048: 128 1126 against 1181).
  *
  * H and I multiples of 64 in [64, 16384]; (N + 1)*H*2, (N + BM)*max(H, I)*4
  * and one expert's codes I*H below 2^31. */

@@ -4,8 +4,11 @@
 // All are HBM-bound passes: every input is read once and every output written
 // once, 8 columns a lane (16 bytes of bf16), so a group of 32 columns is four
 // neighbouring lanes, which share its largest magnitude in two lane swaps.
-// 8192 rows of 7168: 32 us each way, 5.5 TB/s, what a plain copy reaches (two
-// pieces a lane the same, four 33 and 35 us).
+// 8192 rows of 7168, three tensors in turn: 32 us each way in 8 bits, 5.5 TB/s,
+// what a plain copy reaches (two pieces a lane the same, four 33 and 35 us); one
+// after the other, the second from the caches, 37 and 27.  In 4 bits, once in a
+// checkpoint's life, 41 and 37 us (4.0 TB/s: more of it is arithmetic); the
+// weights of 128 experts of 2048 x 768, 1.2 GB, 395 and 354 us.
 #include <algorithm>
 #include <initializer_list>
 
@@ -106,8 +109,8 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint8_t* __res
 // A workgroup takes the rows, one at least, whose 8-column pieces its threads
 // hold at once: lanes have work whatever I is (with a wave a row, I = 64 used
 // one lane in eight: 60000 rows 29 us, 8.8 now), and a thread's loads are all on
-// their way together (32768 rows of 768: 47.5 us, 5.3 TB/s; 53.3 a wave a row,
-// 48.6 with two pieces a thread).  A row is a multiple of 8 pieces: 8
+// their way together (32768 rows of 768, three sets in turn: 47 us, 5.4 TB/s; 53
+// a wave a row, 48.6 with two pieces a thread).  A row is a multiple of 8 pieces: 8
 // neighbouring lanes hold 64 columns of one row, their sum goes to LDS, and 8
 // lanes add a row's sums.  The stores are of the default policy: non-temporal
 // they take this kernel to 42.6 us, but the GEMMs that read d_preact and act

@@ -15,7 +15,7 @@
 //     operand and up to 16 routes as the second.
 //   * A row's scale bytes are loaded for 2048 columns at once and kept in LDS.
 //     Loaded step by step, 8 bytes of each of 64 rows, they took a quarter of
-//     the time (a wide layer's FC1 266 us against 186 without them, 174 now).
+//     the time (a wide layer's FC1 266 us against 186 without them, 173 now).
 //   * A contraction is summed in four parts, added in order.  With few tiles
 //     (w4_split_kernel) the four waves of a workgroup take a part each; with
 //     many (w4_stream_kernel) every wave runs all four for its own rows and
@@ -26,9 +26,11 @@
 //   * The weights' first loads leave as soon as the expert is known, before
 //     the block's row count and tokens are.
 //
-// One token of a layer of 128 experts (8 a token, H 2048, I 768): 11.6 us, FC1
-// 5.6 of them; 16 tokens 30 + 15 us; 128 tokens 44 + 27 us, 4.6 TB/s of weights
-// (a plain read of as many bytes: 34 + 18 us).
+// A layer of 128 experts (8 a token, H 2048, I 768), device time with so many
+// sets of weights in turn that none stays in the caches: one token 14.2 us (FC1
+// 7.4, FC2 and the sum 6.7; 10.4 us when the caches hold the weights), 16 tokens 54
+// us (FC1 31, FC2 18), 128 tokens 79 us (FC1 47, FC2 27: 4.3 TB/s of weights; a
+// plain read of as many bytes takes 34 + 18).
 #include <algorithm>
 #include <initializer_list>
 
@@ -398,8 +400,9 @@ __global__ __launch_bounds__(kW4Waves * kWave) void w4_split_kernel(W4Args p) {
 // through LDS into operand layout, and the next step's loads run beside this
 // step's products.  An operand is read from LDS where it is used and one wave
 // needs few registers, which is what lets four workgroups share a compute unit
-// (three with two route tiles).  128 tokens of the 128-expert layer: FC1 44 us
-// (52 straight to registers), FC2 26 us (32); 256 tokens 48 and 30.  Two steps'
+// (three with two route tiles).  128 tokens of the 128-expert layer, three sets of
+// weights in turn: FC1 45 us (48.6 with the split kernel), FC2 26 us (29.3); 256
+// tokens 48.6 (69) and 30 (45).  Two steps'
 // loads on their way, 64-row waves, waves two by two, eight waves a workgroup
 // and several column tiles a workgroup in turn were no faster.
 template <bool FC1, int WT, bool SALIGN>
@@ -535,9 +538,9 @@ struct W4Stream : W4Rows<FC1, WT, SALIGN> {
     }
 };
 
-// Four waves a SIMD with one route tile (16 tokens: FC1 30 us against 33 with
-// three), three with two (256 tokens of 8 experts of 4096 x 1792: FC1 36.5 us
-// against 42.4 with two).
+// One route tile takes 107 to 111 registers, four waves a SIMD; two are held to
+// three (167 registers instead of 179: 256 tokens of 8 experts of 4096 x 1792 FC1
+// 36.4 us against 43.6, of 128 experts of 2048 x 768 48.6 against 51.6).
 template <bool FC1, int WT, int CTMAX, bool SALIGN>
 __global__ __launch_bounds__(kW4Waves * kWave, CTMAX == 1 ? 4 : 3) void w4_stream_kernel(W4Args p) {
     typedef W4Stream<FC1, WT, SALIGN> Wave;
