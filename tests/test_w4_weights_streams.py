@@ -136,3 +136,27 @@ def test_dropped_tensors_outlive_the_given_stream(handle):
     again = torch.full(shape, 9, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert bool((again == 9).all()) and torch.equal(v, keep.dequantize())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fork", [False, True])
+def test_captured_with_the_stream_given(fork):
+    """On the capturing stream by name, and on another that is joined again;
+    replays follow the inputs."""
+    w = weights(3)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    given = side if fork else main
+    W4Weights.quantize(w).dequantize()                       # the kernels are loaded
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        q = W4Weights.quantize(w, stream=given)
+        v = q.dequantize(stream=given)
+        main.wait_stream(given)
+    for seed in (4, 5, 6):
+        w.copy_(weights(seed))
+        want = W4Weights.quantize(w)
+        back = want.dequantize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales) and torch.equal(v, back)
