@@ -1,5 +1,5 @@
-"""ctypes binding of libmoe_native (the C ABI in include/moe_native.h and
-include/moe_lowbit.h).
+"""ctypes binding of libmoe_native (the C ABI in include/moe_native.h,
+include/moe_lowbit.h and include/moe_block.h).
 
 Argument marshalling only: every function takes torch tensors for the
 device buffers, checks dtype/device/contiguity/size on the host, passes raw
@@ -22,6 +22,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_native.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_native.h")
 LOWBIT_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_lowbit.h")
+BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_block.h")
 PROBE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_probe.h")
 
 if not os.path.exists(LIB_PATH):
@@ -32,6 +33,14 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 _i32, _i64, _f64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor."""
+    _fields_ = [("param", _vp), ("master", _vp), ("grad", _vp), ("m", _vp), ("v", _vp), ("m_scales", _vp),
+                ("v_scales", _vp), ("n", _i64), ("weight_decay", ctypes.c_float), ("param_type", _i32),
+                ("grad_type", _i32), ("reserved", _i32)]
+
 
 _SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -94,6 +103,20 @@ _SIGNATURES = {
     "moe_grouped_fc1_swiglu_save_q8": (ctypes.c_int, [_vp] * 4 + [_i64, _i32, _i32, _i32, _i64]
                                        + [_vp] * 4),
     "moe_swiglu_bwd_q8": (ctypes.c_int, [_vp] * 4 + [_i64, _i32] + [_vp] * 4),
+    "moe_ffn_decode_max_tokens": (_i32, []),
+    "moe_ffn_decode_workspace_bytes": (ctypes.c_size_t, [_i64, _i32, _i32, _i32, _i32]),
+    "moe_ffn_decode": (ctypes.c_int, [_vp] * 6 + [_i64, _i32, _i32, _i32, _i32]
+                       + [_vp] * 3 + [ctypes.c_size_t, _vp, _vp]),
+    "moe_layer_norm_fwd": (ctypes.c_int, [_vp] * 4 + [_i64, _i32, _f64, _i32, _i32] + [_vp] * 5),
+    "moe_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i32]),
+    "moe_layer_norm_bwd": (ctypes.c_int, [_vp] * 6 + [_i64, _i32, _i32, _i32, _i32]
+                           + [_vp] * 4 + [ctypes.c_size_t, _vp]),
+    "moe_grad_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AdamWTensor), _i32]),
+    "moe_grad_norm": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), _i32, _vp, ctypes.c_size_t, _vp, _vp]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), _i32, _i32, _vp, _f64, _f64, _f64, _vp, _f64]
+                       + [_vp] * 3),
+    "moe_moment_values": (ctypes.c_int, [_vp] * 4 + [_i64] + [_vp] * 3),
+    "moe_moment_codes": (ctypes.c_int, [_vp] * 2 + [_i64] + [_vp] * 5),
     "moe_probe_read": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp, _vp]),
     "moe_probe_write": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp]),
     "moe_probe_copy": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp]),
@@ -871,3 +894,223 @@ def moe_swiglu_bwd_q8(codes, scales, d_act, slot_probs, act, d_preact, d_prob, s
         _at(scales, torch.uint8, R * I // 16, "scales", dev), _at(d_act, bf16, 0, "d_act", dev),
         _at(slot_probs, f32, R, "slot_probs", dev), R, I, _at(act, bf16, R * I, "act", dev),
         _at(d_preact, bf16, R * 2 * I, "d_preact", dev), _at(d_prob, f32, R, "d_prob", dev), st))
+
+
+# ------------------------------------------------- operators around the layer
+
+def moe_ffn_decode_max_tokens() -> int:
+    """Most tokens of a moe_ffn_decode call."""
+    return int(lib.moe_ffn_decode_max_tokens())
+
+
+def moe_ffn_decode_workspace_bytes(N: int, H: int, I: int, E: int, K: int) -> int:
+    b = int(lib.moe_ffn_decode_workspace_bytes(N, H, I, E, K))
+    if b == 0:
+        raise MoEError("moe_ffn_decode_workspace_bytes", -2)
+    return b
+
+
+_decode_bytes = functools.lru_cache(maxsize=4096)(moe_ffn_decode_workspace_bytes)
+
+
+def moe_ffn_decode(logits, x, w1, w2, topk_ids, topk_probs, workspace, y, residual=None, n_live=None, stream=None):
+    """The whole layer for up to moe_ffn_decode_max_tokens() tokens, from logits
+    [N, E] to y [N, H] (+ residual): ids, probabilities and y are written."""
+    dev, st = _here_of(x, "x", stream)
+    N, H = x.shape
+    n, E = logits.shape
+    ni, K = topk_ids.shape
+    e1, I2, h1 = w1.shape
+    I = I2 // 2
+    if n != N or ni != N or tuple(topk_probs.shape) != (N, K) or tuple(y.shape) != (N, H):
+        raise ValueError("logits [N, E], topk_ids and topk_probs [N, K], x and y [N, H] must agree in N")
+    if e1 != E or h1 != H or I2 % 2 or tuple(w2.shape) != (E, H, I):
+        raise ValueError("weights must be w1 [E, 2I, H] and w2 [E, H, I] with x [N, H]")
+    bf16 = torch.bfloat16
+    r = 0
+    if residual is not None:
+        if tuple(residual.shape) != (N, H):
+            raise ValueError("residual must be [N, H]")
+        r = _at(residual, bf16, 0, "residual", dev)
+    live = 0 if n_live is None else _at(n_live, torch.int32, 1, "n_live", dev)
+    need = _decode_bytes(N, H, I, E, K)
+    _check("moe_ffn_decode", lib.moe_ffn_decode(
+        _at(logits, torch.float32, 0, "logits", dev), _at(x, bf16, 0, "x", dev), _at(w1, bf16, 0, "w1", dev),
+        _at(w2, bf16, 0, "w2", dev), r, live, N, H, I, E, K, _at(topk_ids, torch.int32, 0, "topk_ids", dev),
+        _at(topk_probs, torch.float32, 0, "topk_probs", dev), _at(workspace, torch.uint8, need, "workspace", dev),
+        workspace.numel(), _at(y, bf16, 0, "y", dev), st))
+
+
+_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _type_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPE:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    return _TYPE[t.dtype]
+
+
+def _matrix(t, name: str, shape, dtype, dev: int) -> int:
+    """Address of a tensor of exactly this shape; 0 for None."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _at(t, dtype, 0, name, dev)
+
+
+def moe_layer_norm_fwd(x, weight, bias, eps: float, y, mean, rstd, residual=None, total=None, stream=None):
+    """y = norm(x + residual) * weight + bias over the last dimension; total, mean and rstd are kept
+    for the backward.  mean None: RMS norm.  total is given with residual, and only then."""
+    xt, yt = _type_of(x, "x"), _type_of(y, "y")
+    if (residual is None) != (total is None):
+        raise ValueError("residual and total must be given together")
+    dev, st = _here_of(x, "x", stream)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    f32 = torch.float32
+    _check("moe_layer_norm_fwd", lib.moe_layer_norm_fwd(
+        _at(x, x.dtype, 0, "x", dev), _matrix(residual, "residual", x.shape, x.dtype, dev),
+        _matrix(weight, "weight", (D,), f32, dev), _matrix(bias, "bias", (D,), f32, dev), rows, D, eps, xt, yt,
+        _matrix(total, "total", x.shape, x.dtype, dev), _matrix(y, "y", x.shape, y.dtype, dev),
+        _matrix(mean, "mean", x.shape[:-1], f32, dev), _matrix(rstd, "rstd", x.shape[:-1], f32, dev), st))
+
+
+def moe_layer_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
+    b = int(lib.moe_layer_norm_bwd_workspace_bytes(rows, D))
+    if b == 0:
+        raise MoEError("moe_layer_norm_bwd_workspace_bytes", -2)
+    return b
+
+
+_norm_bytes = functools.lru_cache(maxsize=4096)(moe_layer_norm_bwd_workspace_bytes)
+
+
+def layer_norm_workspace(rows: int, D: int, device="cuda") -> torch.Tensor:
+    """A device workspace for moe_layer_norm_bwd (uint8)."""
+    return torch.empty(moe_layer_norm_bwd_workspace_bytes(rows, D), dtype=torch.uint8, device=device)
+
+
+def moe_layer_norm_bwd(dy, h, weight, mean, rstd, dx, dweight, dbias, workspace, dtotal=None, accumulate: bool = False,
+                       stream=None):
+    """The backward of moe_layer_norm_fwd: h is what was normalised (total, or x), dtotal the gradient
+    that reaches h past the norm.  dx is written, dweight and dbias (may be None) written or added to."""
+    ht, yt = _type_of(h, "h"), _type_of(dy, "dy")
+    dev, st = _here_of(h, "h", stream)
+    if h.dim() < 1:
+        raise ValueError("h must be [..., D]")
+    D = h.shape[-1]
+    rows = h.numel() // D if D else 0
+    f32 = torch.float32
+    need = _norm_bytes(rows, D)
+    _check("moe_layer_norm_bwd", lib.moe_layer_norm_bwd(
+        _matrix(dy, "dy", h.shape, dy.dtype, dev), _at(h, h.dtype, 0, "h", dev),
+        _matrix(weight, "weight", (D,), f32, dev), _matrix(mean, "mean", h.shape[:-1], f32, dev),
+        _matrix(rstd, "rstd", h.shape[:-1], f32, dev), _matrix(dtotal, "dtotal", h.shape, h.dtype, dev), rows, D,
+        ht, yt, int(bool(accumulate)), _matrix(dx, "dx", h.shape, h.dtype, dev),
+        _matrix(dweight, "dweight", (D,), f32, dev), _matrix(dbias, "dbias", (D,), f32, dev),
+        _at(workspace, torch.uint8, need, "workspace", dev), workspace.numel(), st))
+
+
+class AdamWTable:
+    """The tensors of moe_grad_norm and moe_adamw_step: per tensor its parameter, gradient, moments
+    (codes with scale bytes: 8 bits), master copy and weight decay.  Holds the tensors, so their
+    memory stays theirs; the gradients are the buffers the backward writes."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, masters=None, weight_decay=0.0):
+        count = len(params)
+        lists = dict(grads=grads, m=m, v=v, m_scales=m_scales, v_scales=v_scales, masters=masters)
+        for name, ts in lists.items():
+            if ts is not None and len(ts) != count:
+                raise ValueError(f"{name}: {len(ts)} tensors for {count} parameters")
+        if (m_scales is None) != (v_scales is None):
+            raise ValueError("m_scales and v_scales must be given together")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
+        if len(decay) != count:
+            raise ValueError(f"weight_decay: {len(decay)} values for {count} parameters")
+        self.state = 32 if m_scales is None else 8
+        self.count, self.device = count, None
+        self.tensors = [params] + [ts for ts in lists.values() if ts is not None]
+        self.array = (AdamWTensor * max(count, 1))()
+        for i, p in enumerate(params):
+            pt = _type_of(p, "a parameter")
+            if not p.is_cuda:
+                raise ValueError("a parameter must be a device tensor")
+            if self.device is None:
+                self.device = p.get_device()
+            n, dev, e = p.numel(), self.device, self.array[i]
+            kind = torch.float32 if self.state == 32 else torch.uint8
+            e.param, e.n, e.param_type, e.weight_decay = _at(p, p.dtype, 0, "a parameter", dev), n, pt, decay[i]
+            e.grad_type = _type_of(grads[i], "a gradient")
+            e.grad = self._piece(grads[i], "a gradient", n, grads[i].dtype, dev)
+            e.m, e.v = self._piece(m[i], "a first moment", n, kind, dev), self._piece(v[i], "a second moment", n, kind, dev)
+            if self.state == 8:
+                e.m_scales = self._piece(m_scales[i], "a first moment's scales", -(-n // 32), torch.uint8, dev)
+                e.v_scales = self._piece(v_scales[i], "a second moment's scales", -(-n // 32), torch.uint8, dev)
+            if masters is not None and masters[i] is not None:
+                e.master = self._piece(masters[i], "a master copy", n, torch.float32, dev)
+
+    @staticmethod
+    def _piece(t, name, n, dtype, dev):
+        p = _at(t, dtype, 0, name, dev)
+        if t.numel() != n:
+            raise ValueError(f"{name}: needs {n} elements, has {t.numel()}")
+        return p
+
+    def here(self, stream):
+        dev, st = _here(stream)
+        if self.device is not None and dev != self.device:
+            raise ValueError(f"the tensors are on cuda:{self.device}, the current device is cuda:{dev}")
+        return dev, st
+
+
+def moe_grad_norm_workspace_bytes(table: AdamWTable) -> int:
+    b = int(lib.moe_grad_norm_workspace_bytes(table.array, table.count))
+    if b == 0:
+        raise MoEError("moe_grad_norm_workspace_bytes", -2)
+    return b
+
+
+def moe_grad_norm(table: AdamWTable, workspace, norm, stream=None):
+    """norm (float32 [1]) = the 2-norm of all gradients of the table."""
+    dev, st = table.here(stream)
+    _check("moe_grad_norm", lib.moe_grad_norm(
+        table.array, table.count, _at(workspace, torch.uint8, 0, "workspace", dev), workspace.numel(),
+        _at(norm, torch.float32, 1, "norm", dev), st))
+
+
+def moe_adamw_step(table: AdamWTable, lr, betas, eps: float, step, ticket, grad_norm=None, max_norm: float = 0.0,
+                   stream=None):
+    """One AdamW step of the table's tensors.  lr float32 [1], step int32 [1] (moved on), ticket int32
+    [1] (0 between calls), grad_norm float32 [1] or None: device scalars."""
+    dev, st = table.here(stream)
+    _check("moe_adamw_step", lib.moe_adamw_step(
+        table.array, table.count, table.state, _at(lr, torch.float32, 1, "lr", dev), betas[0], betas[1], eps,
+        0 if grad_norm is None else _at(grad_norm, torch.float32, 1, "grad_norm", dev), max_norm,
+        _at(step, torch.int32, 1, "step", dev), _at(ticket, torch.int32, 1, "ticket", dev), st))
+
+
+def moe_moment_values(m, m_scales, v, v_scales, m_values, root_values, stream=None):
+    """What 8-bit moments stand for: m and the root of v, bf16, of a whole tensor's n elements."""
+    dev, st = _here_of(m, "m", stream)
+    n, u8, bf16 = m.numel(), torch.uint8, torch.bfloat16
+    groups = -(-n // 32)
+    _check("moe_moment_values", lib.moe_moment_values(
+        _at(m, u8, n, "m", dev), _at(m_scales, u8, groups, "m_scales", dev), _at(v, u8, n, "v", dev),
+        _at(v_scales, u8, groups, "v_scales", dev), n, _at(m_values, bf16, n, "m_values", dev),
+        _at(root_values, bf16, n, "root_values", dev), st))
+
+
+def moe_moment_codes(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
+    """8-bit moments from float32 ones of a whole tensor."""
+    dev, st = _here_of(m, "m", stream)
+    n, f32, u8 = m.numel(), torch.float32, torch.uint8
+    groups = -(-n // 32)
+    _check("moe_moment_codes", lib.moe_moment_codes(
+        _at(m, f32, n, "m", dev), _at(v, f32, n, "v", dev), n, _at(m_codes, u8, n, "m_codes", dev),
+        _at(m_scales, u8, groups, "m_scales", dev), _at(v_codes, u8, n, "v_codes", dev),
+        _at(v_scales, u8, groups, "v_scales", dev), st))

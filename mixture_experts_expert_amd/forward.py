@@ -290,3 +290,34 @@ def forward_dropless(buf: DroplessBuffers, logits, x, w1, w2, stream=None):
     buf.grouped_ffn(x, w1, w2, stream)
     buf.combine(stream)
     return buf.y
+
+
+class DecodeBuffers:
+    """Device buffers for forward_decode: up to N tokens (at most
+    moe_ffn_decode_max_tokens()) of one layer shape."""
+
+    def __init__(self, N: int, H: int, I: int, E: int, K: int, device="cuda"):
+        self.N, self.H, self.I, self.E, self.K = N, H, I, E, K
+        need = nat.moe_ffn_decode_workspace_bytes(N, H, I, E, K)      # refuses what is not served
+        dev = torch.device(device)
+        self.topk_ids = torch.zeros((N, K), dtype=torch.int32, device=dev)
+        self.topk_probs = torch.zeros((N, K), dtype=torch.float32, device=dev)
+        self.y = torch.zeros((N, H), dtype=torch.bfloat16, device=dev)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def forward_decode(buf: DecodeBuffers, logits, x, w1, w2, residual=None, n_live=None, stream=None):
+    """The dropless forward for the few tokens of a decode step, in two kernels
+    on bf16 weights: n = x.shape[0] <= buf.N tokens, residual (bf16 [n, H])
+    added to their sums.  Returns buf.y[:n]; topk_ids[:n] and topk_probs[:n]
+    hold the routing.  n_live (device int32 [1]): rows at or past it are not
+    computed and keep what they held."""
+    n = x.shape[0]
+    if n > buf.N:
+        raise ValueError(f"{n} tokens, the buffers hold {buf.N}")
+    if n == buf.N:
+        ids, probs, y = buf.topk_ids, buf.topk_probs, buf.y
+    else:
+        ids, probs, y = buf.topk_ids[:n], buf.topk_probs[:n], buf.y[:n]
+    nat.moe_ffn_decode(logits, x, w1, w2, ids, probs, buf.workspace, y, residual, n_live, stream)
+    return y
