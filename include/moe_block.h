@@ -124,8 +124,8 @@ int moe_layer_norm_bwd(const void* dy, const void* h, const float* weight, const
  * Gradient norm and AdamW over many tensors
  * ------------------------------------------------------------------------ */
 
-/* One tensor of n elements.  Pointers are device pointers; the array of these
- * is read on the host during the call and not kept. */
+/* One tensor of n elements.  Pointers are device pointers; an array of these is
+ * read on the host during a call and not kept. */
 typedef struct {
     void* param;            /* bf16 or float32 [n], updated                         */
     float* master;          /* float32 [n], updated, param then its rounding; null:
@@ -133,9 +133,9 @@ typedef struct {
     const void* grad;       /* bf16 or float32 [n]                                  */
     void* m;                /* first moment: float32 [n], or codes uint8 [n]        */
     void* v;                /* second moment: float32 [n], or codes uint8 [n]       */
-    uint8_t* m_scales;      /* 8 bits: ceil(n / 32) scale bytes each; else null     */
-    uint8_t* v_scales;
-    int64_t n;              /* elements, 0 and up                                   */
+    uint8_t* m_scales;      /* codes: ceil(n / 32) scale bytes each, of any         */
+    uint8_t* v_scales;      /* alignment; null for float32 moments                  */
+    int64_t n;              /* elements, 0 to 2^34                                  */
     float weight_decay;
     int32_t param_type;     /* moe_dtype                                            */
     int32_t grad_type;      /* moe_dtype                                            */
@@ -154,13 +154,21 @@ typedef struct {
  * The scale is the smallest b >= 1 with which no magnitude of the group rounds
  * past the largest code (464 and 1.96875 times 2^(b-127) go to the next b). */
 
-/* Bytes of moe_grad_norm's workspace for these tensors (0: bad arguments). */
-size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor* tensors, int32_t count);
+/* A plan: a device buffer that holds the list of tensors for the kernels, and
+ * their partial sums and counters.  moe_adamw_plan writes it (with kernels, no
+ * copy); moe_grad_norm and moe_adamw_step take the same list again, on the
+ * host, and the plan written for it: as long as the tensors stay where they
+ * are, one plan serves every step.  Calls that share a plan must not overlap.
+ * All tensors of a list have moments of the same kind; together at most 2^40
+ * elements.  0 bytes: bad arguments. */
+size_t moe_adamw_plan_bytes(const moe_adamw_tensor* tensors, int32_t count);
+int moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                   hipStream_t stream);
 
 /* norm[0] = float32( sqrt( sum over all tensors of grad^2 ) ): squares and sums
- * in float64, in a fixed order.  Reads grad, grad_type and n alone. */
-int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* workspace,
-                  size_t workspace_bytes, float* norm, hipStream_t stream);
+ * in float64, in a fixed order. */
+int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                  float* norm, hipStream_t stream);
 
 /* One AdamW step of every tensor:
  *   c = max_norm / norm where norm > max_norm, else 1 (and 1 without grad_norm)
@@ -174,16 +182,12 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* workspac
  *   grad_norm  in  float32 [1], device scalar (moe_grad_norm's); may be null.
  *                  Not finite: the call leaves everything as it was, step included
  *   max_norm   > 0, used with grad_norm only
- *   state      32 or 8: bits of every tensor's moments
  *   step       in/out int32 [1], device scalar: steps taken so far; becomes t
- *   ticket     in/out uint32 [1], device scalar, 0 before the first call and
- *                  left 0 by each: counts the workgroups that are done.  Calls
- *                  that share step or ticket must not overlap
  *
  * 0 <= beta < 1, eps >= 0.  No two tensors may share memory that is written. */
-int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t state, const float* lr,
-                   double beta1, double beta2, double eps, const float* grad_norm, double max_norm,
-                   int32_t* step, uint32_t* ticket, hipStream_t stream);
+int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                   const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
+                   double max_norm, int32_t* step, hipStream_t stream);
 
 /* What 8-bit moments stand for: m and the root of v, both bf16 [n] (exact from
  * b = 13 on; below, where bf16 ends, rounded to its subnormals).

@@ -111,10 +111,10 @@ _SIGNATURES = {
     "moe_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i32]),
     "moe_layer_norm_bwd": (ctypes.c_int, [_vp] * 6 + [_i64, _i32, _i32, _i32, _i32]
                            + [_vp] * 4 + [ctypes.c_size_t, _vp]),
-    "moe_grad_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AdamWTensor), _i32]),
-    "moe_grad_norm": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), _i32, _vp, ctypes.c_size_t, _vp, _vp]),
-    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), _i32, _i32, _vp, _f64, _f64, _f64, _vp, _f64]
-                       + [_vp] * 3),
+    "moe_adamw_plan_bytes": (ctypes.c_size_t, [_vp, _i32]),
+    "moe_adamw_plan": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp]),
+    "moe_grad_norm": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp, _vp]),
+    "moe_adamw_step": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp, _f64, _f64, _f64, _vp, _f64, _vp, _vp]),
     "moe_moment_values": (ctypes.c_int, [_vp] * 4 + [_i64] + [_vp] * 3),
     "moe_moment_codes": (ctypes.c_int, [_vp] * 2 + [_i64] + [_vp] * 5),
     "moe_probe_read": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp, _vp]),
@@ -917,28 +917,26 @@ def moe_ffn_decode(logits, x, w1, w2, topk_ids, topk_probs, workspace, y, residu
     """The whole layer for up to moe_ffn_decode_max_tokens() tokens, from logits
     [N, E] to y [N, H] (+ residual): ids, probabilities and y are written."""
     dev, st = _here_of(x, "x", stream)
-    N, H = x.shape
+    shape = x.shape
+    N, H = shape
     n, E = logits.shape
     ni, K = topk_ids.shape
     e1, I2, h1 = w1.shape
     I = I2 // 2
-    if n != N or ni != N or tuple(topk_probs.shape) != (N, K) or tuple(y.shape) != (N, H):
+    if n != N or ni != N or topk_probs.shape != (N, K) or y.shape != shape:
         raise ValueError("logits [N, E], topk_ids and topk_probs [N, K], x and y [N, H] must agree in N")
-    if e1 != E or h1 != H or I2 % 2 or tuple(w2.shape) != (E, H, I):
+    if e1 != E or h1 != H or I2 % 2 or w2.shape != (E, H, I):
         raise ValueError("weights must be w1 [E, 2I, H] and w2 [E, H, I] with x [N, H]")
     bf16 = torch.bfloat16
-    r = 0
-    if residual is not None:
-        if tuple(residual.shape) != (N, H):
-            raise ValueError("residual must be [N, H]")
-        r = _at(residual, bf16, 0, "residual", dev)
-    live = 0 if n_live is None else _at(n_live, torch.int32, 1, "n_live", dev)
-    need = _decode_bytes(N, H, I, E, K)
-    _check("moe_ffn_decode", lib.moe_ffn_decode(
+    status = lib.moe_ffn_decode(
         _at(logits, torch.float32, 0, "logits", dev), _at(x, bf16, 0, "x", dev), _at(w1, bf16, 0, "w1", dev),
-        _at(w2, bf16, 0, "w2", dev), r, live, N, H, I, E, K, _at(topk_ids, torch.int32, 0, "topk_ids", dev),
-        _at(topk_probs, torch.float32, 0, "topk_probs", dev), _at(workspace, torch.uint8, need, "workspace", dev),
-        workspace.numel(), _at(y, bf16, 0, "y", dev), st))
+        _at(w2, bf16, 0, "w2", dev), _like(residual, "residual", shape, bf16, dev),
+        0 if n_live is None else _at(n_live, torch.int32, 1, "n_live", dev), N, H, I, E, K,
+        _at(topk_ids, torch.int32, 0, "topk_ids", dev), _at(topk_probs, torch.float32, 0, "topk_probs", dev),
+        _at(workspace, torch.uint8, _decode_bytes(N, H, I, E, K), "workspace", dev), workspace.numel(),
+        _at(y, bf16, 0, "y", dev), st)
+    if status:
+        raise MoEError("moe_ffn_decode", status)
 
 
 _TYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -952,13 +950,32 @@ def _type_of(t, name: str) -> int:
     return _TYPE[t.dtype]
 
 
-def _matrix(t, name: str, shape, dtype, dev: int) -> int:
+def _like(t, name: str, shape, dtype, dev: int) -> int:
     """Address of a tensor of exactly this shape; 0 for None."""
     if t is None:
         return 0
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return _at(t, dtype, 0, name, dev)
+
+
+def _vector(t, name: str, n: int, dev: int) -> int:
+    """Address of a float32 tensor of n elements; 0 for None."""
+    if t is None:
+        return 0
+    try:
+        if t.numel() == n and t.dtype is torch.float32 and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, has {t.numel()}")
+    return _at(t, torch.float32, 0, name, dev)
 
 
 def moe_layer_norm_fwd(x, weight, bias, eps: float, y, mean, rstd, residual=None, total=None, stream=None):
@@ -968,16 +985,17 @@ def moe_layer_norm_fwd(x, weight, bias, eps: float, y, mean, rstd, residual=None
     if (residual is None) != (total is None):
         raise ValueError("residual and total must be given together")
     dev, st = _here_of(x, "x", stream)
-    if x.dim() < 1:
+    shape, dt = x.shape, x.dtype
+    if not shape:
         raise ValueError("x must be [..., D]")
-    D = x.shape[-1]
+    D = shape[-1]
     rows = x.numel() // D if D else 0
-    f32 = torch.float32
-    _check("moe_layer_norm_fwd", lib.moe_layer_norm_fwd(
-        _at(x, x.dtype, 0, "x", dev), _matrix(residual, "residual", x.shape, x.dtype, dev),
-        _matrix(weight, "weight", (D,), f32, dev), _matrix(bias, "bias", (D,), f32, dev), rows, D, eps, xt, yt,
-        _matrix(total, "total", x.shape, x.dtype, dev), _matrix(y, "y", x.shape, y.dtype, dev),
-        _matrix(mean, "mean", x.shape[:-1], f32, dev), _matrix(rstd, "rstd", x.shape[:-1], f32, dev), st))
+    status = lib.moe_layer_norm_fwd(
+        _at(x, dt, 0, "x", dev), _like(residual, "residual", shape, dt, dev), _vector(weight, "weight", D, dev),
+        _vector(bias, "bias", D, dev), rows, D, eps, xt, yt, _like(total, "total", shape, dt, dev),
+        _like(y, "y", shape, y.dtype, dev), _vector(mean, "mean", rows, dev), _vector(rstd, "rstd", rows, dev), st)
+    if status:
+        raise MoEError("moe_layer_norm_fwd", status)
 
 
 def moe_layer_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
@@ -1001,27 +1019,28 @@ def moe_layer_norm_bwd(dy, h, weight, mean, rstd, dx, dweight, dbias, workspace,
     that reaches h past the norm.  dx is written, dweight and dbias (may be None) written or added to."""
     ht, yt = _type_of(h, "h"), _type_of(dy, "dy")
     dev, st = _here_of(h, "h", stream)
-    if h.dim() < 1:
+    shape, dt = h.shape, h.dtype
+    if not shape:
         raise ValueError("h must be [..., D]")
-    D = h.shape[-1]
+    D = shape[-1]
     rows = h.numel() // D if D else 0
-    f32 = torch.float32
-    need = _norm_bytes(rows, D)
-    _check("moe_layer_norm_bwd", lib.moe_layer_norm_bwd(
-        _matrix(dy, "dy", h.shape, dy.dtype, dev), _at(h, h.dtype, 0, "h", dev),
-        _matrix(weight, "weight", (D,), f32, dev), _matrix(mean, "mean", h.shape[:-1], f32, dev),
-        _matrix(rstd, "rstd", h.shape[:-1], f32, dev), _matrix(dtotal, "dtotal", h.shape, h.dtype, dev), rows, D,
-        ht, yt, int(bool(accumulate)), _matrix(dx, "dx", h.shape, h.dtype, dev),
-        _matrix(dweight, "dweight", (D,), f32, dev), _matrix(dbias, "dbias", (D,), f32, dev),
-        _at(workspace, torch.uint8, need, "workspace", dev), workspace.numel(), st))
+    status = lib.moe_layer_norm_bwd(
+        _like(dy, "dy", shape, dy.dtype, dev), _at(h, dt, 0, "h", dev), _vector(weight, "weight", D, dev),
+        _vector(mean, "mean", rows, dev), _vector(rstd, "rstd", rows, dev), _like(dtotal, "dtotal", shape, dt, dev),
+        rows, D, ht, yt, 1 if accumulate else 0, _like(dx, "dx", shape, dt, dev), _vector(dweight, "dweight", D, dev),
+        _vector(dbias, "dbias", D, dev), _at(workspace, torch.uint8, _norm_bytes(rows, D), "workspace", dev),
+        workspace.numel(), st)
+    if status:
+        raise MoEError("moe_layer_norm_bwd", status)
 
 
 class AdamWTable:
-    """The tensors of moe_grad_norm and moe_adamw_step: per tensor its parameter, gradient, moments
-    (codes with scale bytes: 8 bits), master copy and weight decay.  Holds the tensors, so their
-    memory stays theirs; the gradients are the buffers the backward writes."""
+    """The tensors of moe_grad_norm and moe_adamw_step and their plan: per tensor its parameter,
+    gradient, moments (codes with scale bytes: 8 bits), master copy and weight decay.  Holds the
+    tensors, so their memory stays theirs; the gradients are the buffers the backward writes.  The
+    plan is written on `stream` (None: the current one)."""
 
-    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, masters=None, weight_decay=0.0):
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, masters=None, weight_decay=0.0, stream=None):
         count = len(params)
         lists = dict(grads=grads, m=m, v=v, m_scales=m_scales, v_scales=v_scales, masters=masters)
         for name, ts in lists.items():
@@ -1029,69 +1048,88 @@ class AdamWTable:
                 raise ValueError(f"{name}: {len(ts)} tensors for {count} parameters")
         if (m_scales is None) != (v_scales is None):
             raise ValueError("m_scales and v_scales must be given together")
+        if not count:
+            raise ValueError("no parameters")
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
         if len(decay) != count:
             raise ValueError(f"weight_decay: {len(decay)} values for {count} parameters")
-        self.state = 32 if m_scales is None else 8
-        self.count, self.device = count, None
-        self.tensors = [params] + [ts for ts in lists.values() if ts is not None]
-        self.array = (AdamWTensor * max(count, 1))()
-        for i, p in enumerate(params):
-            pt = _type_of(p, "a parameter")
-            if not p.is_cuda:
-                raise ValueError("a parameter must be a device tensor")
-            if self.device is None:
-                self.device = p.get_device()
-            n, dev, e = p.numel(), self.device, self.array[i]
-            kind = torch.float32 if self.state == 32 else torch.uint8
-            e.param, e.n, e.param_type, e.weight_decay = _at(p, p.dtype, 0, "a parameter", dev), n, pt, decay[i]
-            e.grad_type = _type_of(grads[i], "a gradient")
-            e.grad = self._piece(grads[i], "a gradient", n, grads[i].dtype, dev)
-            e.m, e.v = self._piece(m[i], "a first moment", n, kind, dev), self._piece(v[i], "a second moment", n, kind, dev)
-            if self.state == 8:
-                e.m_scales = self._piece(m_scales[i], "a first moment's scales", -(-n // 32), torch.uint8, dev)
-                e.v_scales = self._piece(v_scales[i], "a second moment's scales", -(-n // 32), torch.uint8, dev)
-            if masters is not None and masters[i] is not None:
-                e.master = self._piece(masters[i], "a master copy", n, torch.float32, dev)
-
-    @staticmethod
-    def _piece(t, name, n, dtype, dev):
-        p = _at(t, dtype, 0, name, dev)
-        if t.numel() != n:
-            raise ValueError(f"{name}: needs {n} elements, has {t.numel()}")
-        return p
+        self.count, kind = count, torch.float32 if m_scales is None else torch.uint8
+        none = [None] * count
+        self.tensors = list(zip(params, masters or none, grads, m, v, m_scales or none, v_scales or none))
+        for t in self.tensors:
+            _type_of(t[0], "a parameter")
+            _type_of(t[2], "a gradient")
+        self.device, st = _here_of(params[0], "a parameter", stream)
+        dev, f32, u8 = self.device, torch.float32, torch.uint8
+        self.array = (AdamWTensor * count)()
+        for e, (p, master, g, a, b, sa, sb), wd in zip(self.array, self.tensors, decay):
+            n = p.numel()
+            e.param, e.n, e.weight_decay = _at(p, p.dtype, 0, "a parameter", dev), n, wd
+            e.param_type, e.grad_type = _TYPE[p.dtype], _TYPE[g.dtype]
+            e.grad = _whole(g, "a gradient", n, g.dtype, dev)
+            e.m, e.v = _whole(a, "a first moment", n, kind, dev), _whole(b, "a second moment", n, kind, dev)
+            if kind is u8:
+                e.m_scales = _whole(sa, "a first moment's scales", -(-n // 32), u8, dev)
+                e.v_scales = _whole(sb, "a second moment's scales", -(-n // 32), u8, dev)
+            if master is not None:
+                e.master = _whole(master, "a master copy", n, f32, dev)
+        self.address = ctypes.addressof(self.array)
+        self.bytes = int(lib.moe_adamw_plan_bytes(self.address, count))
+        if self.bytes == 0:
+            raise MoEError("moe_adamw_plan_bytes", -2)
+        self.plan = torch.empty(self.bytes, dtype=torch.uint8, device=params[0].device)
+        if stream is not None:
+            _hand_over(stream, self.plan)
+        self.plan_at = self.plan.data_ptr()
+        _check("moe_adamw_plan", lib.moe_adamw_plan(self.address, count, self.plan_at, self.bytes, st))
 
     def here(self, stream):
         dev, st = _here(stream)
-        if self.device is not None and dev != self.device:
+        if dev != self.device:
             raise ValueError(f"the tensors are on cuda:{self.device}, the current device is cuda:{dev}")
         return dev, st
 
 
-def moe_grad_norm_workspace_bytes(table: AdamWTable) -> int:
-    b = int(lib.moe_grad_norm_workspace_bytes(table.array, table.count))
-    if b == 0:
-        raise MoEError("moe_grad_norm_workspace_bytes", -2)
-    return b
+def _whole(t, name, n, dtype, dev):
+    p = _at(t, dtype, 0, name, dev)
+    if t.numel() != n:
+        raise ValueError(f"{name}: needs {n} elements, has {t.numel()}")
+    return p
 
 
-def moe_grad_norm(table: AdamWTable, workspace, norm, stream=None):
+def _hand_over(stream, *tensors: torch.Tensor):
+    """Order `stream` (None: the current one) behind the current stream, where
+    the fresh outputs among `tensors` were allocated: work pending there may
+    still write their blocks.  The allocator learns that `stream` uses them
+    all, so that none is handed out again too early."""
+    if stream is None:
+        return
+    t = tensors[0]
+    _here_of(t, "the tensor", stream)                 # refusals come first
+    if not hasattr(stream, "wait_stream"):            # a raw handle
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    stream.wait_stream(torch.cuda.current_stream(t.device))
+    for t in tensors:
+        t.record_stream(stream)
+
+
+def moe_grad_norm(table: AdamWTable, norm, stream=None):
     """norm (float32 [1]) = the 2-norm of all gradients of the table."""
     dev, st = table.here(stream)
     _check("moe_grad_norm", lib.moe_grad_norm(
-        table.array, table.count, _at(workspace, torch.uint8, 0, "workspace", dev), workspace.numel(),
-        _at(norm, torch.float32, 1, "norm", dev), st))
+        table.address, table.count, table.plan_at, table.bytes, _at(norm, torch.float32, 1, "norm", dev), st))
 
 
-def moe_adamw_step(table: AdamWTable, lr, betas, eps: float, step, ticket, grad_norm=None, max_norm: float = 0.0,
+def moe_adamw_step(table: AdamWTable, lr, betas, eps: float, step, grad_norm=None, max_norm: float = 0.0,
                    stream=None):
-    """One AdamW step of the table's tensors.  lr float32 [1], step int32 [1] (moved on), ticket int32
-    [1] (0 between calls), grad_norm float32 [1] or None: device scalars."""
+    """One AdamW step of the table's tensors.  lr float32 [1], step int32 [1] (moved on) and grad_norm
+    float32 [1] (or None) are device scalars."""
     dev, st = table.here(stream)
+    f32 = torch.float32
     _check("moe_adamw_step", lib.moe_adamw_step(
-        table.array, table.count, table.state, _at(lr, torch.float32, 1, "lr", dev), betas[0], betas[1], eps,
-        0 if grad_norm is None else _at(grad_norm, torch.float32, 1, "grad_norm", dev), max_norm,
-        _at(step, torch.int32, 1, "step", dev), _at(ticket, torch.int32, 1, "ticket", dev), st))
+        table.address, table.count, table.plan_at, table.bytes, _at(lr, f32, 1, "lr", dev), betas[0], betas[1], eps,
+        0 if grad_norm is None else _at(grad_norm, f32, 1, "grad_norm", dev), max_norm,
+        _at(step, torch.int32, 1, "step", dev), st))
 
 
 def moe_moment_values(m, m_scales, v, v_scales, m_values, root_values, stream=None):

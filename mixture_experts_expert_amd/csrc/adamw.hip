@@ -5,9 +5,11 @@
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // HBM-bound: every byte of state is read and written once.  Tensors are cut
-// into chunks of a fixed length, a workgroup a chunk, and a launch takes up to
-// kBatch tensors, whose table travels in the kernel's arguments: no table to
-// upload, nothing to keep, and a captured call replays what it was given.
+// into chunks, a workgroup a chunk, and one launch takes all of them whatever
+// their sizes: a plan in device memory names each chunk's tensor, so a
+// workgroup finds its work in two dependent loads.  (A table in the kernel's
+// arguments takes 44 tensors a launch and is read from host memory: 300 small
+// tensors 14 launches, 104 us.)
 #include <math.h>
 
 #include <algorithm>
@@ -25,124 +27,191 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
-constexpr int kEach = 4;                             // elements of a lane's piece
-constexpr int kPieces = 4;                           // pieces of a lane
+constexpr int kEach = 8;                             // elements of a lane's piece
+constexpr int kPieces = 2;                           // pieces of a lane
 constexpr int kChunk = kThreads * kEach * kPieces;   // elements of a workgroup
-constexpr int kNormPieces = 16;
-constexpr int kNormChunk = kThreads * kEach * kNormPieces;
-constexpr int kBatch = 44;                           // tensors of a launch (the arguments hold 4 KB)
+constexpr int kBatch = 44;                           // entries of a launch that writes a plan (arguments hold 4 KB)
+constexpr int kNormBlocks = 2048;                    // workgroups of the norm, at most: eight a compute unit
 constexpr int64_t kMaxBlocks = int64_t(1) << 23;     // workgroups of a launch: a grid holds under 2^32 threads
-constexpr int64_t kMaxElements = int64_t(1) << 34;
+constexpr int64_t kMaxElements = int64_t(1) << 34;   // of a tensor
+constexpr int64_t kMaxChunks = int64_t(1) << 28;     // of all
 
-struct AdamWEntry {
+// A chunk: its pieces of a tensor.
+struct Chunk {
     void* param;
     float* master;
     const void* grad;
     void *m, *v;
     uint8_t *m_scales, *v_scales;
-    int64_t n;
-    float weight_decay;
+    int32_t n;                                       // elements, up to kChunk
     int32_t types;                                   // bit 0: float32 param, bit 1: float32 gradient
+    float weight_decay;
+    int32_t pad;
+};
+static_assert(sizeof(Chunk) == 72, "layout");
+
+// Counts the workgroups of a launch that are done.  Atomics on one address take
+// turns, so workgroups count in kGroups groups, and the last of a group counts
+// for it.  Every counter has its cache lines to itself: with the chunks beside it
+// each atomic took them from the other XCDs' caches (75 M elements 1590 us
+// against 390).
+struct Line {
+    uint32_t n, pad[31];
+};
+constexpr uint32_t kGroups = 32;
+struct Counter {
+    Line group[kGroups], all;
+    __device__ __forceinline__ void reset() {
+        for (uint32_t i = 0; i < kGroups; ++i) group[i].n = 0u;
+        all.n = 0u;
+    }
+    // Whether this workgroup is the last of `total` to come here; leaves zeros then.
+    __device__ __forceinline__ bool last(uint32_t me, uint32_t total) {
+        const uint32_t g = me % kGroups, members = (total - g + kGroups - 1) / kGroups;
+        if (count(&group[g].n) != members - 1) return false;
+        clear(&group[g].n);
+        if (count(&all.n) != min(total, kGroups) - 1) return false;
+        clear(&all.n);
+        return true;
+    }
+    static __device__ __forceinline__ uint32_t count(uint32_t* p) {
+        return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    static __device__ __forceinline__ void clear(uint32_t* p) {
+        __hip_atomic_store(p, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 };
 
-struct AdamWBatch {
-    AdamWEntry e[kBatch];
-    int32_t first[kBatch];                           // first workgroup of each tensor; INT32_MAX past the last
-    const float* lr;
-    const float* grad_norm;
-    int32_t* step;
-    uint32_t* ticket;                                // null: not the last launch
-    double log2_beta1, log2_beta2;                   // -inf for beta 0
-    float beta1, beta2, one_less_beta1, one_less_beta2, eps, max_norm;
+// A plan: the norm's partial sums, the counters, then the chunks.
+struct PlanHead {
+    double part[kNormBlocks];
+    Counter norm_done, step_done;
 };
-static_assert(sizeof(AdamWBatch) <= 4096, "kernel arguments");
-
-struct GradBatch {
-    const void* grad[kBatch];
-    int64_t n[kBatch];
-    int32_t first[kBatch];
-    int32_t f32[kBatch];
-    double* part;                                    // of this launch's first workgroup
+static_assert(sizeof(PlanHead) % 128 == 0, "whole lines");
+struct Plan {
+    PlanHead* head;
+    __host__ __device__ Chunk* chunk() const { return reinterpret_cast<Chunk*>(head + 1); }
 };
 
-// The tensor of a workgroup: the last one that begins at or before it.
-__device__ __forceinline__ int find_tensor(const int32_t* first) {
-    const int lane = lane_id();
-    const int f = lane < kBatch ? first[lane] : INT32_MAX;
-    const uint64_t begun = __ballot(f <= static_cast<int>(blockIdx.x));
-    return __builtin_amdgcn_readfirstlane(static_cast<int>(__popcll(begun)) - 1);
+// Writing it: up to kBatch tensors a launch, a workgroup each.
+struct Entry {
+    Chunk all;                                       // (all.n is not used)
+    int64_t n;
+    int32_t first;                                   // chunk
+    int32_t state;
+};
+struct PlanBatch {
+    Entry e[kBatch];
+};
+static_assert(sizeof(PlanBatch) + 8 <= 4096, "kernel arguments");
+
+__global__ void plan_reset_kernel(PlanHead* head) {
+    head->norm_done.reset();
+    head->step_done.reset();
 }
 
-// Elements i .. i+3 of a tensor of n; those past the end are 0.
-__device__ __forceinline__ floatx4 load4(const float* p, int64_t i, int64_t n) {
-    if (i + kEach <= n) return *reinterpret_cast<const floatx4*>(p + i);
-    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+__global__ __launch_bounds__(kThreads) void plan_kernel(PlanBatch b, Plan plan) {
+    const Entry e = b.e[blockIdx.x];
+    const int32_t chunks = static_cast<int32_t>((e.n + kChunk - 1) / kChunk);
+    for (int32_t i = threadIdx.x; i < chunks; i += kThreads) {
+        const int64_t at = static_cast<int64_t>(i) * kChunk;
+        auto bytes_on = [&](auto* p, int size) {
+            return reinterpret_cast<decltype(p)>(reinterpret_cast<uintptr_t>(p) + (p ? at * size : 0));
+        };
+        const int state = e.state == 8 ? 1 : 4;
+        Chunk c = e.all;
+        c.param = bytes_on(c.param, c.types & 1 ? 4 : 2);
+        c.master = bytes_on(c.master, 4);
+        c.grad = bytes_on(c.grad, c.types & 2 ? 4 : 2);
+        c.m = bytes_on(c.m, state);
+        c.v = bytes_on(c.v, state);
+        if (c.m_scales) c.m_scales += at / kGroup;
+        if (c.v_scales) c.v_scales += at / kGroup;
+        c.n = static_cast<int32_t>(e.n - at < kChunk ? e.n - at : kChunk);
+        plan.chunk()[e.first + i] = c;
+    }
+}
+
+// Elements i .. i+7 of n, as two halves; those past the end are 0.
+struct Eight {
+    floatx4 h[2];
+    __device__ __forceinline__ float& operator[](int j) { return reinterpret_cast<float*>(h)[j]; }
+    __device__ __forceinline__ float operator[](int j) const { return reinterpret_cast<const float*>(h)[j]; }
+};
+__device__ __forceinline__ Eight load8(const float* p, int i, int n) {
+    Eight v;
+    if (i + kEach <= n) {
+        v.h[0] = reinterpret_cast<const floatx4*>(p + i)[0];
+        v.h[1] = reinterpret_cast<const floatx4*>(p + i)[1];
+        return v;
+    }
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
-        if (i + j < n) v[j] = p[i + j];
+    for (int j = 0; j < kEach; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
     return v;
 }
-__device__ __forceinline__ floatx4 load4(const uint16_t* p, int64_t i, int64_t n) {
-    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ Eight load8(const uint16_t* p, int i, int n) {
+    Eight v;
     if (i + kEach <= n) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(p + i);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p + i);
 #pragma unroll
         for (int j = 0; j < kEach; ++j) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
         return v;
     }
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
-        if (i + j < n) v[j] = bf16_to_f32(p[i + j]);
+    for (int j = 0; j < kEach; ++j) v[j] = i + j < n ? bf16_to_f32(p[i + j]) : 0.0f;
     return v;
 }
-__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n) {
-    if (i + kEach <= n) return *reinterpret_cast<const uint32_t*>(p + i);
-    uint32_t v = 0;
+__device__ __forceinline__ u32x2 load8(const uint8_t* p, int i, int n) {
+    if (i + kEach <= n) return *reinterpret_cast<const u32x2*>(p + i);
+    u32x2 v = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-        if (i + j < n) v |= static_cast<uint32_t>(p[i + j]) << (8 * j);
+        if (i + j < n) v[j / 4] |= static_cast<uint32_t>(p[i + j]) << (8 * (j % 4));
     return v;
 }
-__device__ __forceinline__ floatx4 load4_as(const void* p, bool f32, int64_t i, int64_t n) {
-    return f32 ? load4(static_cast<const float*>(p), i, n) : load4(static_cast<const uint16_t*>(p), i, n);
+__device__ __forceinline__ Eight load8_as(const void* p, bool f32, int i, int n) {
+    return f32 ? load8(static_cast<const float*>(p), i, n) : load8(static_cast<const uint16_t*>(p), i, n);
 }
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, floatx4 v) {
+__device__ __forceinline__ void store8(float* p, int i, int n, const Eight& v) {
     if (i + kEach <= n) {
-        *reinterpret_cast<floatx4*>(p + i) = v;
+        reinterpret_cast<floatx4*>(p + i)[0] = v.h[0];
+        reinterpret_cast<floatx4*>(p + i)[1] = v.h[1];
         return;
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
         if (i + j < n) p[i + j] = v[j];
 }
-__device__ __forceinline__ void store4(uint16_t* p, int64_t i, int64_t n, floatx4 v) {
+__device__ __forceinline__ void store8(uint16_t* p, int i, int n, const Eight& v) {
     if (i + kEach <= n) {
-        u32x2 w;
-        w[0] = pack_bf16x2(v[0], v[1]);
-        w[1] = pack_bf16x2(v[2], v[3]);
-        *reinterpret_cast<u32x2*>(p + i) = w;
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < kEach; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]);
+        *reinterpret_cast<u32x4*>(p + i) = w;
         return;
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
         if (i + j < n) p[i + j] = f32_to_bf16(v[j]);
 }
-__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, uint32_t v) {
+__device__ __forceinline__ void store8(uint8_t* p, int i, int n, u32x2 v) {
     if (i + kEach <= n) {
-        *reinterpret_cast<uint32_t*>(p + i) = v;
+        *reinterpret_cast<u32x2*>(p + i) = v;
         return;
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-        if (i + j < n) p[i + j] = static_cast<uint8_t>(v >> (8 * j));
+        if (i + j < n) p[i + j] = static_cast<uint8_t>(v[j / 4] >> (8 * (j % 4)));
 }
 
 // ---------------------------------------------------------------- moments in 8 bits
-// A group of 32 elements is 8 neighbouring lanes' pieces.
+// A group of 32 elements is 4 neighbouring lanes' pieces.
 
 // The largest magnitude's bits over a group (NaN above infinity above numbers).
-__device__ __forceinline__ uint32_t group_max(floatx4 v) {
-    uint32_t m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+__device__ __forceinline__ uint32_t group_max(const Eight& v) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) m = max(m, abs_bits(v[j]));
 #pragma unroll
     for (int o = 1; o < kGroup / kEach; o <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o)));
     return m;
@@ -150,45 +219,60 @@ __device__ __forceinline__ uint32_t group_max(floatx4 v) {
 
 // e4m3: 448 = 1.75 * 2^8 is the largest, 464 = 1.8125 * 2^8 would round past it.
 __device__ __forceinline__ int first_scale(uint32_t amax) { return scale_byte<0x180000u, 8>(amax); }
-__device__ __forceinline__ uint32_t first_codes(floatx4 v, int b) {
+__device__ __forceinline__ u32x2 first_codes(const Eight& v, int b) {
     const float inv = inv_scale(b);
-    int w = 0;
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, w, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
-    return b == kScaleNaN ? 0u : static_cast<uint32_t>(w);
+    u32x2 o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, w, true);
+        o[i] = b == kScaleNaN ? 0u : static_cast<uint32_t>(w);
+    }
+    return o;
 }
-__device__ __forceinline__ floatx4 first_values(uint32_t w, uint32_t b) {
+__device__ __forceinline__ Eight first_values(u32x2 w, uint32_t b) {
     const float s = scale_value(b);
-    floatx4 v;
-    v[0] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 0) * s;
-    v[1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 1) * s;
-    v[2] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 2) * s;
-    v[3] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 3) * s;
+    Eight v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = static_cast<int>(w[i]);
+        v[4 * i] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * s;
+        v[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(c, 1) * s;
+        v[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(c, 2) * s;
+        v[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(c, 3) * s;
+    }
     return v;
 }
 
 // Unsigned e4m4 without subnormals: the exponent and the upper four bits of the
 // mantissa of a float in [2^-15, 2), counted from 2^-15 on; code 0 is 0.
 __device__ __forceinline__ int root_scale(uint32_t amax) { return scale_byte<0x40000u, 0>(amax); }
-__device__ __forceinline__ uint32_t root_code(float r, float inv) {
-    const int bits = __float_as_int(r * inv);
-    const int c = ((bits + 0x3FFFF + (bits >> 19 & 1)) >> 19) - 112 * 16;
-    return r > 0.0f ? static_cast<uint32_t>(max(c, 1)) : 0u;
-}
-__device__ __forceinline__ uint32_t root_codes(floatx4 r, int b) {
+__device__ __forceinline__ u32x2 root_codes(const Eight& r, int b) {
     const float inv = inv_scale(b);
-    const uint32_t w = root_code(r[0], inv) | root_code(r[1], inv) << 8 | root_code(r[2], inv) << 16 | root_code(r[3], inv) << 24;
-    return b == kScaleNaN ? 0u : w;
-}
-__device__ __forceinline__ floatx4 root_values(uint32_t w, uint32_t b) {
-    const float s = scale_value(b);
-    floatx4 v;
+    u32x2 o = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        const uint32_t c = w >> (8 * j) & 255u;
+        const int bits = __float_as_int(r[j] * inv);
+        const int c = ((bits + 0x3FFFF + (bits >> 19 & 1)) >> 19) - 112 * 16;
+        o[j / 4] |= (r[j] > 0.0f ? static_cast<uint32_t>(max(c, 1)) : 0u) << (8 * (j % 4));
+    }
+    return b == kScaleNaN ? u32x2{0u, 0u} : o;
+}
+__device__ __forceinline__ Eight root_values(u32x2 w, uint32_t b) {
+    const float s = scale_value(b);
+    Eight v;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const uint32_t c = w[j / 4] >> (8 * (j % 4)) & 255u;
         v[j] = (c ? __uint_as_float((c << 19) + (112u << 23)) : 0.0f) * s;
     }
     return v;
+}
+
+// The hardware's root (1 ulp), which takes no subnormals: those are scaled up first.
+__device__ __forceinline__ float root_of(float v) {
+    const bool low = v < 0x1p-96f;
+    return __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v) * (low ? 0x1p-32f : 1.0f);
 }
 
 // ---------------------------------------------------------------- gradient norm
@@ -196,6 +280,7 @@ __device__ __forceinline__ floatx4 root_values(uint32_t w, uint32_t b) {
 __device__ __forceinline__ double block_sum(double v, double* s_part) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+    __syncthreads();
     if (lane_id() == 0) s_part[threadIdx.x / kWave] = v;
     __syncthreads();
     double t = 0.0;
@@ -203,80 +288,158 @@ __device__ __forceinline__ double block_sum(double v, double* s_part) {
     return t;
 }
 
-__global__ __launch_bounds__(kThreads) void grad_square_kernel(GradBatch b) {
-    __shared__ double s_part[kThreads / kWave];
-    const int k = find_tensor(b.first);
-    const int64_t n = b.n[k], base = static_cast<int64_t>(static_cast<int>(blockIdx.x) - b.first[k]) * kNormChunk;
-    const bool f32 = b.f32[k] != 0;
-    const void* g = b.grad[k];
-    double s[kEach] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-    for (int i = 0; i < kNormPieces; ++i) {
-        const floatx4 v = load4_as(g, f32, base + (i * kThreads + static_cast<int>(threadIdx.x)) * kEach, n);
+// Waits until the wave's memory operations have been performed.
+__device__ __forceinline__ void wait_memory() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// Eight squares are added in float32 and their sum in float64, unless it leaves
+// float32's range: conversions and float64 products of every element would take
+// longer than a bf16 gradient's bytes.
+__device__ __forceinline__ double squares(const float (&v)[8]) {
+    float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) s[j] += static_cast<double>(v[j]) * static_cast<double>(v[j]);
-    }
-    const double t = block_sum((s[0] + s[1]) + (s[2] + s[3]), s_part);
-    if (threadIdx.x == 0) b.part[blockIdx.x] = t;
+    for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+    if (s > 1e-25f && s < 1e38f) return static_cast<double>(s);
+    double d = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d += static_cast<double>(v[j]) * static_cast<double>(v[j]);
+    return d;
 }
 
-constexpr int kFinishThreads = 1024;
-__global__ __launch_bounds__(kFinishThreads) void grad_norm_kernel(const double* __restrict__ part, int64_t n,
-                                                                   float* __restrict__ norm) {
-    __shared__ double s_part[kFinishThreads / kWave];
+// A workgroup squares the gradients of a run of chunks, 16 bytes a lane and load,
+// the next chunk on its way; the last workgroup to finish adds the sums of all in
+// their order.  The sums pass between the XCDs' caches as device-scope atomics,
+// which are performed in memory: a sum is there before its workgroup counts
+// itself, and is read there.
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(Plan plan, int chunks, float* __restrict__ norm) {
+    __shared__ double s_part[kThreads / kWave];
+    __shared__ bool s_last;
+    constexpr int PIECES = kChunk * 4 / (kThreads * 16);          // of a float32 chunk, 16 bytes each; half of them in bf16
+    const int G = gridDim.x, t = threadIdx.x;
+    const int share = chunks / G, over = chunks - share * G, b0 = blockIdx.x;
+    const int lo = b0 * share + min(b0, over), hi = lo + share + (b0 < over ? 1 : 0);
+    u32x4 next[PIECES], now[PIECES];
+    bool f32 = false;
+    auto load = [&](int c) {
+        const Chunk& k = plan.chunk()[c];
+        f32 = (k.types & 2) != 0;
+        const uint8_t* g = static_cast<const uint8_t*>(k.grad);
+        const int bytes = k.n * (f32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int at = (i * kThreads + t) * 16;
+            next[i] = u32x4{0u, 0u, 0u, 0u};
+            if (at + 16 <= bytes) {
+                next[i] = *reinterpret_cast<const u32x4*>(g + at);
+            } else if (at < bytes) {                              // the last piece of a tensor, by its elements
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at + 2 * j < bytes)
+                        next[i][j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(g + at + 2 * j)) << (16 * (j % 2));
+            }
+        }
+    };
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kFinishThreads) s += part[i];
-    s = block_sum(s, s_part);
-    if (threadIdx.x == 0) norm[0] = static_cast<float>(sqrt(s));
+    if (lo < hi) load(lo);
+    for (int c = lo; c < hi; ++c) {
+        const bool wide = f32;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) now[i] = next[i];
+        if (c + 1 < hi) load(c + 1);
+#pragma unroll
+        for (int i = 0; i < PIECES; i += 2) {
+            float v[8];
+            if (wide) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(now[i + j / 4][j % 4]);
+                s += squares(v);
+            } else if (i < PIECES / 2) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = __uint_as_float(j & 1 ? now[i + h][j / 2] & 0xFFFF0000u : now[i + h][j / 2] << 16);
+                    s += squares(v);
+                }
+            }
+        }
+    }
+    const double sum = block_sum(s, s_part);
+    if (t == 0) {
+        __hip_atomic_store(&plan.head->part[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        wait_memory();
+        s_last = plan.head->norm_done.last(blockIdx.x, G);
+    }
+    __syncthreads();
+    if (!s_last) return;
+    double all = 0.0;
+    for (int i = t; i < G; i += kThreads)
+        all += __hip_atomic_load(&plan.head->part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    all = block_sum(all, s_part);
+    if (t == 0) norm[0] = static_cast<float>(sqrt(all));
 }
 
 // ---------------------------------------------------------------- AdamW
 
-// One piece: the moments and the parameter's new value.
+struct AdamWArgs {
+    Plan plan;
+    const float* lr;
+    const float* grad_norm;
+    int32_t* step;
+    double log2_beta1, log2_beta2;                   // -inf for beta 0
+    float beta1, beta2, one_less_beta1, one_less_beta2, eps, max_norm;
+    int chunk0, chunks;                              // this launch's first chunk, all launches' chunks
+};
+
 struct AdamWScalars {
     float clip, beta1, beta2, one_less_beta1, one_less_beta2, eps, keep, rate, inv_root_bc2;
-    __device__ __forceinline__ void update(floatx4 g, floatx4& m, floatx4& v, floatx4& root, floatx4& p) const {
+    // One piece: the moments, the second one's root and the parameter's new value.
+    __device__ __forceinline__ void update(const Eight& g, Eight& m, Eight& v, Eight& root, Eight& p) const {
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             const float x = g[j] * clip;
             m[j] = beta1 * m[j] + one_less_beta1 * x;
             v[j] = beta2 * v[j] + one_less_beta2 * x * x;
-            root[j] = __builtin_sqrtf(v[j]);
-            p[j] = p[j] * keep - rate * (m[j] / (root[j] * inv_root_bc2 + eps));
+            root[j] = root_of(v[j]);
+            p[j] = p[j] * keep - rate * m[j] * __builtin_amdgcn_rcpf(root[j] * inv_root_bc2 + eps);
         }
     }
 };
 
+// A workgroup a chunk: all its loads are issued before the scalars are looked at.
 template <bool Q8>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWBatch b) {
-    const float norm = b.grad_norm ? b.grad_norm[0] : 0.0f;
-    // infinite or NaN: nothing is written, the step is not taken
-    if ((__float_as_uint(norm) & 0x7F800000u) == 0x7F800000u) return;
-    const int t = __builtin_amdgcn_readfirstlane(b.step[0]) + 1;
-    const int k = find_tensor(b.first);
-    if (k >= 0) {                                    // (a launch of empty tensors alone has none)
-        const AdamWEntry& e = b.e[k];
-        const int64_t n = e.n, base = static_cast<int64_t>(static_cast<int>(blockIdx.x) - b.first[k]) * kChunk;
-        const bool f32 = (e.types & 1) != 0, g32 = (e.types & 2) != 0;
-        floatx4 g[kPieces], p[kPieces], m[kPieces], v[kPieces];
-        uint32_t mc[kPieces], vc[kPieces], mb[kPieces], vb[kPieces];
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
+    const int c = b.chunk0 + static_cast<int>(blockIdx.x);
+    const bool there = c < b.chunks;                 // (without any element one workgroup moves the step alone)
+    const Chunk& e = b.plan.chunk()[there ? c : 0];
+    const int n = there ? e.n : 0;
+    const bool f32 = there && (e.types & 1) != 0, g32 = there && (e.types & 2) != 0;
+    Eight g[kPieces], p[kPieces], m[kPieces], v[kPieces];
+    u32x2 mc[kPieces], vc[kPieces];
+    uint32_t mb[kPieces], vb[kPieces];
+    if (there) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int64_t at = base + (i * kThreads + static_cast<int>(threadIdx.x)) * kEach;
-            g[i] = load4_as(e.grad, g32, at, n);
-            p[i] = e.master ? load4(e.master, at, n) : load4_as(e.param, f32, at, n);
+            const int at = (i * kThreads + static_cast<int>(threadIdx.x)) * kEach;
+            g[i] = load8_as(e.grad, g32, at, n);
+            p[i] = e.master ? load8(e.master, at, n) : load8_as(e.param, f32, at, n);
             if (Q8) {
-                mc[i] = load4(static_cast<const uint8_t*>(e.m), at, n);
-                vc[i] = load4(static_cast<const uint8_t*>(e.v), at, n);
+                mc[i] = load8(static_cast<const uint8_t*>(e.m), at, n);
+                vc[i] = load8(static_cast<const uint8_t*>(e.v), at, n);
                 mb[i] = at < n ? e.m_scales[at / kGroup] : 1;
                 vb[i] = at < n ? e.v_scales[at / kGroup] : 1;
             } else {
-                m[i] = load4(static_cast<const float*>(e.m), at, n);
-                v[i] = load4(static_cast<const float*>(e.v), at, n);
+                m[i] = load8(static_cast<const float*>(e.m), at, n);
+                v[i] = load8(static_cast<const float*>(e.v), at, n);
             }
         }
+    }
+    const float norm = b.grad_norm ? b.grad_norm[0] : 0.0f;
+    const float lr = b.lr[0];
+    const int t = __builtin_amdgcn_readfirstlane(b.step[0]) + 1;
+    // infinite or NaN: nothing is written, the step is not taken
+    if ((__float_as_uint(norm) & 0x7F800000u) == 0x7F800000u) return;
+    if (there) {
         AdamWScalars s;
-        const float lr = b.lr[0];
         const double bc1 = 1.0 - exp2(t * b.log2_beta1), bc2 = 1.0 - exp2(t * b.log2_beta2);
         s.clip = norm > b.max_norm ? b.max_norm / norm : 1.0f;
         s.beta1 = b.beta1; s.beta2 = b.beta2;
@@ -287,81 +450,75 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWBatch b) {
         s.inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int64_t at = base + (i * kThreads + static_cast<int>(threadIdx.x)) * kEach;
+            const int at = (i * kThreads + static_cast<int>(threadIdx.x)) * kEach;
             if (Q8) {
                 m[i] = first_values(mc[i], mb[i]);
                 v[i] = root_values(vc[i], vb[i]);
-                v[i] *= v[i];
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) v[i][j] *= v[i][j];
             }
-            floatx4 root;
+            Eight root;
             s.update(g[i], m[i], v[i], root, p[i]);
             if (Q8) {
                 // elements past the end are zeros and take no part in the scale
                 const int bm = first_scale(group_max(m[i])), br = root_scale(group_max(root));
-                store4(static_cast<uint8_t*>(e.m), at, n, first_codes(m[i], bm));
-                store4(static_cast<uint8_t*>(e.v), at, n, root_codes(root, br));
+                store8(static_cast<uint8_t*>(e.m), at, n, first_codes(m[i], bm));
+                store8(static_cast<uint8_t*>(e.v), at, n, root_codes(root, br));
                 if (at < n && at % kGroup == 0) {
                     e.m_scales[at / kGroup] = static_cast<uint8_t>(bm);
                     e.v_scales[at / kGroup] = static_cast<uint8_t>(br);
                 }
             } else {
-                store4(static_cast<float*>(e.m), at, n, m[i]);
-                store4(static_cast<float*>(e.v), at, n, v[i]);
+                store8(static_cast<float*>(e.m), at, n, m[i]);
+                store8(static_cast<float*>(e.v), at, n, v[i]);
             }
-            if (e.master) store4(e.master, at, n, p[i]);
-            if (f32) store4(static_cast<float*>(e.param), at, n, p[i]);
-            else store4(static_cast<uint16_t*>(e.param), at, n, p[i]);
+            if (e.master) store8(e.master, at, n, p[i]);
+            if (f32) store8(static_cast<float*>(e.param), at, n, p[i]);
+            else store8(static_cast<uint16_t*>(e.param), at, n, p[i]);
         }
     }
-    // all waves of a workgroup have read the step when it counts itself; the last
-    // one to do so moves it
-    if (!b.ticket) return;
+    // All waves of a workgroup have read the step when it counts itself; the last
+    // one of the last launch moves it.
+    if (b.chunk0 + static_cast<int>(gridDim.x) < b.chunks) return;
     __syncthreads();
-    if (threadIdx.x == 0 && atomicAdd(b.ticket, 1u) == gridDim.x - 1) {
-        b.step[0] = t;
-        b.ticket[0] = 0u;
-    }
+    if (threadIdx.x == 0 && b.plan.head->step_done.last(blockIdx.x, gridDim.x)) b.step[0] = t;
 }
 
+// Workgroup x: elements from x * kThreads * kEach on.
+constexpr int kSpan = kThreads * kEach;
 __global__ __launch_bounds__(kThreads) void moment_values_kernel(const uint8_t* __restrict__ m, const uint8_t* __restrict__ ms,
                                                                  const uint8_t* __restrict__ v, const uint8_t* __restrict__ vs,
                                                                  int64_t n, uint16_t* __restrict__ mo, uint16_t* __restrict__ ro) {
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kEach;
-    if (at >= n) return;
-    store4(mo, at, n, first_values(load4(m, at, n), ms[at / kGroup]));
-    store4(ro, at, n, root_values(load4(v, at, n), vs[at / kGroup]));
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kSpan;
+    const int at = threadIdx.x * kEach, left = static_cast<int>(min(n - base, static_cast<int64_t>(kSpan)));
+    if (at >= left) return;
+    const u32x2 a = load8(m + base, at, left), c = load8(v + base, at, left);
+    const int64_t group = (base + at) / kGroup;
+    store8(mo + base, at, left, first_values(a, ms[group]));
+    store8(ro + base, at, left, root_values(c, vs[group]));
 }
 
 __global__ __launch_bounds__(kThreads) void moment_codes_kernel(const float* __restrict__ m, const float* __restrict__ v,
                                                                 int64_t n, uint8_t* __restrict__ mc, uint8_t* __restrict__ ms,
                                                                 uint8_t* __restrict__ vc, uint8_t* __restrict__ vs) {
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kEach;
-    const floatx4 a = load4(m, at, n);
-    floatx4 r = load4(v, at, n);
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kSpan;
+    const int at = threadIdx.x * kEach, left = static_cast<int>(min(n - base, static_cast<int64_t>(kSpan)));
+    const Eight a = load8(m + base, at, left);
+    Eight r = load8(v + base, at, left);
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) r[j] = __builtin_sqrtf(r[j]);
+    for (int j = 0; j < kEach; ++j) r[j] = root_of(r[j]);
     const int bm = first_scale(group_max(a)), br = root_scale(group_max(r));
-    store4(mc, at, n, first_codes(a, bm));
-    store4(vc, at, n, root_codes(r, br));
-    if (at < n && at % kGroup == 0) {
-        ms[at / kGroup] = static_cast<uint8_t>(bm);
-        vs[at / kGroup] = static_cast<uint8_t>(br);
+    store8(mc + base, at, left, first_codes(a, bm));
+    store8(vc + base, at, left, root_codes(r, br));
+    if (at < left && at % kGroup == 0) {
+        ms[(base + at) / kGroup] = static_cast<uint8_t>(bm);
+        vs[(base + at) / kGroup] = static_cast<uint8_t>(br);
     }
 }
 
 // ---------------------------------------------------------------- host side
 
 bool is_type(int32_t t) { return t == MOE_BF16 || t == MOE_F32; }
-int64_t chunks(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
-
-int check_list(const moe_adamw_tensor* t, int32_t count) {
-    if (count < 0 || (count > 0 && !t)) return MOE_ERR_INVALID_ARG;
-    for (int i = 0; i < count; ++i) {
-        if (t[i].n < 0 || !is_type(t[i].grad_type) || t[i].reserved != 0) return MOE_ERR_INVALID_ARG;
-        if (t[i].n > kMaxElements) return MOE_ERR_UNSUPPORTED;
-    }
-    return MOE_OK;
-}
 
 int check_pointers(std::initializer_list<const void*> ptrs) {
     for (const void* q : ptrs)
@@ -372,105 +529,122 @@ int check_pointers(std::initializer_list<const void*> ptrs) {
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// What a list comes to: chunks, tensors that hold something, bits of their moments.
+struct ListShape {
+    int64_t chunks = 0;
+    int entries = 0, state = 32;
+    size_t bytes() const { return sizeof(PlanHead) + static_cast<size_t>(std::max<int64_t>(chunks, 1)) * sizeof(Chunk); }
+};
+
+int check_list(const moe_adamw_tensor* t, int32_t count, ListShape* s) {
+    if (count < 0 || (count > 0 && !t)) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (t[i].n < 0) return MOE_ERR_INVALID_ARG;
+        if (t[i].n > kMaxElements) return MOE_ERR_UNSUPPORTED;
+        if (t[i].n == 0) continue;
+        const int state = t[i].m_scales ? 8 : 32;
+        if (!t[i].m_scales != !t[i].v_scales || (s->entries > 0 && state != s->state)) return MOE_ERR_INVALID_ARG;
+        s->state = state;
+        s->chunks += (t[i].n + kChunk - 1) / kChunk;
+        ++s->entries;
+        if (s->chunks > kMaxChunks) return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+// The plan that goes with a list.
+int check_plan(const moe_adamw_tensor* t, int32_t count, const void* plan, size_t bytes, ListShape* s) {
+    const int st = check_list(t, count, s);
+    if (st != MOE_OK) return st;
+    if (!plan || bytes < s->bytes()) return MOE_ERR_INVALID_ARG;
+    return aligned16(plan) ? MOE_OK : MOE_ERR_MISALIGNED;
+}
+
 }  // namespace
 }  // namespace moe
 
-extern "C" size_t moe_grad_norm_workspace_bytes(const moe_adamw_tensor* tensors, int32_t count) {
-    if (moe::check_list(tensors, count) != MOE_OK) return 0;
-    int64_t n = 0;
-    for (int i = 0; i < count; ++i) n += moe::chunks(tensors[i].n, moe::kNormChunk);
-    return static_cast<size_t>(std::max<int64_t>(n, 2)) * sizeof(double);
+extern "C" size_t moe_adamw_plan_bytes(const moe_adamw_tensor* tensors, int32_t count) {
+    moe::ListShape s;
+    return moe::check_list(tensors, count, &s) == MOE_OK ? s.bytes() : 0;
 }
 
-extern "C" int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* workspace,
-                             size_t workspace_bytes, float* norm, hipStream_t stream) {
+extern "C" int moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                              hipStream_t stream) {
     using namespace moe;
-    int st = check_list(tensors, count);
+    ListShape s;
+    int st = check_plan(tensors, count, plan, plan_bytes, &s);
     if (st != MOE_OK) return st;
-    for (int i = 0; i < count; ++i)
-        if (tensors[i].n > 0 && (st = check_pointers({tensors[i].grad})) != MOE_OK) return st;
-    st = check_pointers({workspace});
-    if (st != MOE_OK) return st;
-    if (!norm || workspace_bytes < moe_grad_norm_workspace_bytes(tensors, count)) return MOE_ERR_INVALID_ARG;
-    if (!aligned4(norm)) return MOE_ERR_MISALIGNED;
-    int64_t total = 0;
-    GradBatch b;
-    int used = 0;
-    int64_t blocks = 0;
-    auto flush = [&]() {
-        if (!used) return;
-        for (int i = used; i < kBatch; ++i) b.first[i] = INT32_MAX;
-        b.part = static_cast<double*>(workspace) + total;
-        grad_square_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(b);
-        total += blocks;
-        used = 0;
-        blocks = 0;
-    };
     for (int i = 0; i < count; ++i) {
-        const int64_t c = chunks(tensors[i].n, kNormChunk);
-        if (c == 0) continue;
-        if (used == kBatch || blocks + c > kMaxBlocks) flush();
-        b.grad[used] = tensors[i].grad;
-        b.n[used] = tensors[i].n;
-        b.f32[used] = tensors[i].grad_type;
-        b.first[used++] = static_cast<int32_t>(blocks);
-        blocks += c;
+        const moe_adamw_tensor& t = tensors[i];
+        if (!is_type(t.param_type) || !is_type(t.grad_type) || t.reserved != 0 || !std::isfinite(t.weight_decay))
+            return MOE_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if ((st = check_pointers({t.param, t.grad, t.m, t.v})) != MOE_OK) return st;
+        if (!aligned16(t.master)) return MOE_ERR_MISALIGNED;
     }
-    flush();
-    grad_norm_kernel<<<1, kFinishThreads, 0, stream>>>(static_cast<const double*>(workspace), total, norm);
+    const Plan p = Plan{static_cast<PlanHead*>(plan)};
+    PlanBatch b{};
+    int used = 0;
+    int32_t chunk = 0;
+    plan_reset_kernel<<<1, 1, 0, stream>>>(p.head);
+    for (int i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n > 0) {
+            b.e[used++] = Entry{Chunk{t.param, t.master, t.grad, t.m, t.v, t.m_scales, t.v_scales, 0,
+                                      (t.param_type == MOE_F32 ? 1 : 0) | (t.grad_type == MOE_F32 ? 2 : 0), t.weight_decay, 0},
+                                t.n, chunk, s.state};
+            chunk += static_cast<int32_t>((t.n + kChunk - 1) / kChunk);
+        }
+        if (used == kBatch || (i == count - 1 && used > 0)) {
+            plan_kernel<<<used, kThreads, 0, stream>>>(b, p);
+            used = 0;
+        }
+    }
     return launch_status();
 }
 
-extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t state, const float* lr,
-                              double beta1, double beta2, double eps, const float* grad_norm, double max_norm,
-                              int32_t* step, uint32_t* ticket, hipStream_t stream) {
+extern "C" int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                             float* norm, hipStream_t stream) {
     using namespace moe;
-    int st = check_list(tensors, count);
+    ListShape s;
+    const int st = check_plan(tensors, count, plan, plan_bytes, &s);
+    if (st != MOE_OK) return st;
+    if (!norm) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(norm)) return MOE_ERR_MISALIGNED;
+    const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(s.chunks, 1), kNormBlocks));
+    grad_norm_kernel<<<grid, kThreads, 0, stream>>>(Plan{static_cast<PlanHead*>(plan)}, static_cast<int>(s.chunks), norm);
+    return launch_status();
+}
+
+extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                              const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
+                              double max_norm, int32_t* step, hipStream_t stream) {
+    using namespace moe;
+    ListShape s;
+    const int st = check_plan(tensors, count, plan, plan_bytes, &s);
     if (st != MOE_OK) return st;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
         (grad_norm && !(max_norm > 0.0)))
         return MOE_ERR_INVALID_ARG;
-    if (state != 32 && state != 8) return MOE_ERR_INVALID_ARG;
-    if (!lr || !step || !ticket) return MOE_ERR_INVALID_ARG;
-    if (!aligned4(lr) || !aligned4(step) || !aligned4(ticket) || !aligned4(grad_norm)) return MOE_ERR_MISALIGNED;
-    for (int i = 0; i < count; ++i) {
-        const moe_adamw_tensor& t = tensors[i];
-        if (!is_type(t.param_type) || !std::isfinite(t.weight_decay)) return MOE_ERR_INVALID_ARG;
-        if (t.n == 0) continue;
-        if ((st = check_pointers({t.param, t.grad, t.m, t.v})) != MOE_OK) return st;
-        if (t.master && !aligned16(t.master)) return MOE_ERR_MISALIGNED;
-        if (state == 8 ? !t.m_scales || !t.v_scales : t.m_scales || t.v_scales) return MOE_ERR_INVALID_ARG;
-    }
-    AdamWBatch b;
-    b.lr = lr; b.grad_norm = grad_norm; b.step = step;
-    b.log2_beta1 = std::log2(beta1); b.log2_beta2 = std::log2(beta2);
-    b.beta1 = static_cast<float>(beta1); b.beta2 = static_cast<float>(beta2);
-    b.one_less_beta1 = static_cast<float>(1.0 - beta1); b.one_less_beta2 = static_cast<float>(1.0 - beta2);
-    b.eps = static_cast<float>(eps);
-    b.max_norm = grad_norm ? static_cast<float>(max_norm) : 0.0f;
-    int used = 0;
-    int64_t blocks = 0;
-    auto flush = [&](bool last) {
-        if (!used && !last) return;
-        for (int i = used; i < kBatch; ++i) b.first[i] = INT32_MAX;
-        b.ticket = last ? ticket : nullptr;
-        const unsigned g = static_cast<unsigned>(std::max<int64_t>(blocks, 1));
-        if (state == 8) adamw_kernel<true><<<g, kThreads, 0, stream>>>(b);
-        else adamw_kernel<false><<<g, kThreads, 0, stream>>>(b);
-        used = 0;
-        blocks = 0;
-    };
-    for (int i = 0; i < count; ++i) {
-        const moe_adamw_tensor& t = tensors[i];
-        const int64_t c = chunks(t.n, kChunk);
-        if (c == 0) continue;
-        if (used == kBatch || blocks + c > kMaxBlocks) flush(false);
-        b.e[used] = AdamWEntry{t.param, t.master, t.grad, t.m, t.v, t.m_scales, t.v_scales, t.n, t.weight_decay,
-                               (t.param_type == MOE_F32 ? 1 : 0) | (t.grad_type == MOE_F32 ? 2 : 0)};
-        b.first[used++] = static_cast<int32_t>(blocks);
-        blocks += c;
-    }
-    flush(true);
+    if (!lr || !step) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(lr) || !aligned4(step) || !aligned4(grad_norm)) return MOE_ERR_MISALIGNED;
+    AdamWArgs a;
+    a.plan = Plan{static_cast<PlanHead*>(plan)};
+    a.lr = lr; a.grad_norm = grad_norm; a.step = step;
+    a.log2_beta1 = std::log2(beta1); a.log2_beta2 = std::log2(beta2);
+    a.beta1 = static_cast<float>(beta1); a.beta2 = static_cast<float>(beta2);
+    a.one_less_beta1 = static_cast<float>(1.0 - beta1); a.one_less_beta2 = static_cast<float>(1.0 - beta2);
+    a.eps = static_cast<float>(eps);
+    a.max_norm = grad_norm ? static_cast<float>(max_norm) : 0.0f;
+    a.chunks = static_cast<int>(s.chunks);
+    int64_t at = 0;
+    do {
+        const unsigned grid = static_cast<unsigned>(std::min(std::max<int64_t>(s.chunks - at, 1), kMaxBlocks));
+        a.chunk0 = static_cast<int>(at);
+        if (s.state == 8) adamw_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+        else adamw_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+        at += grid;
+    } while (at < s.chunks);
     return launch_status();
 }
 

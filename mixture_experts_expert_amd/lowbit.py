@@ -11,22 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import _native as nat
-
-
-def _hand_over(stream, *tensors: torch.Tensor):
-    """Order `stream` (None: the current one) behind the current stream, where
-    the fresh outputs among `tensors` were allocated: work pending there may
-    still write their blocks.  The allocator learns that `stream` uses them
-    all, so that none is handed out again too early."""
-    if stream is None:
-        return
-    t = tensors[0]
-    nat._here_of(t, "the tensor", stream)             # refusals come first
-    if not hasattr(stream, "wait_stream"):            # a raw handle
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    stream.wait_stream(torch.cuda.current_stream(t.device))
-    for t in tensors:
-        t.record_stream(stream)
+from ._native import _hand_over
 
 
 class W4Weights:

@@ -1,10 +1,9 @@
 """AdamW over many tensors at once, clipped by the gradients' global norm.
 
 The gradients are buffers that the backward writes (a MoEBackwardBuffers'
-main_dw1 and main_dw2, a norm's dweight), so a step is three launches for any
-number of tensors up to a few dozen, reads nothing back and can be captured
-into a hipGraph with the backward: the learning rate and the number of the
-step are device scalars.  All arithmetic runs in libmoe_native's kernels.
+main_dw1 and main_dw2, a norm's dweight), so a step is two launches for any
+number of tensors, reads nothing back and can be captured into a hipGraph with
+the backward: the learning rate and the number of the step are device scalars.  All arithmetic runs in libmoe_native's kernels.
 """
 
 from __future__ import annotations
@@ -67,17 +66,14 @@ class MoEAdamW:
         self.lr = lr if isinstance(lr, torch.Tensor) else torch.full((1,), float(lr), device=dev)
         self.step = step if isinstance(step, torch.Tensor) else torch.full((1,), int(step), dtype=torch.int32, device=dev)
         self.norm = torch.zeros(1, device=dev)
-        self.ticket = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.workspace = torch.empty(nat.moe_grad_norm_workspace_bytes(self.table), dtype=torch.uint8, device=dev)
 
     def step_(self, stream=None):
         """Clip and step: every parameter, moment and master copy, in place."""
         if self.max_norm is None:
-            nat.moe_adamw_step(self.table, self.lr, self.betas, self.eps, self.step, self.ticket, stream=stream)
+            nat.moe_adamw_step(self.table, self.lr, self.betas, self.eps, self.step, stream=stream)
             return
-        nat.moe_grad_norm(self.table, self.workspace, self.norm, stream)
-        nat.moe_adamw_step(self.table, self.lr, self.betas, self.eps, self.step, self.ticket, self.norm,
-                           self.max_norm, stream)
+        nat.moe_grad_norm(self.table, self.norm, stream)
+        nat.moe_adamw_step(self.table, self.lr, self.betas, self.eps, self.step, self.norm, self.max_norm, stream)
 
     def moment_values(self, i: int, stream=None):
         """What parameter i's moments stand for: (m, root of v) in bf16 for 8-bit

@@ -19,11 +19,11 @@ def test_every_declared_symbol_is_exported_with_its_arguments():
     names = moe.header_functions(moe.BLOCK_HEADER_PATH)
     assert set(names) == {"moe_ffn_decode_max_tokens", "moe_ffn_decode_workspace_bytes", "moe_ffn_decode",
                           "moe_layer_norm_fwd", "moe_layer_norm_bwd_workspace_bytes", "moe_layer_norm_bwd",
-                          "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adamw_step", "moe_moment_values",
-                          "moe_moment_codes"}
+                          "moe_adamw_plan_bytes", "moe_adamw_plan", "moe_grad_norm", "moe_adamw_step",
+                          "moe_moment_values", "moe_moment_codes"}
     text = re.sub(r"/\*.*?\*/", "", open(moe.BLOCK_HEADER_PATH).read(), flags=re.S)
     for n in names:
-        assert hasattr(lib, n) and n in nat._SIGNATURES and hasattr(moe, n), n
+        assert hasattr(lib, n) and n in nat._SIGNATURES, n
         args = re.search(r"\b%s\s*\((.*?)\)\s*;" % n, text, flags=re.S).group(1)
         declared = 0 if args.strip() == "void" else len(args.split(","))
         assert declared == len(nat._SIGNATURES[n][1]), n
@@ -99,28 +99,38 @@ def table(n=8, **kw):
 
 
 def test_adamw_validation():
-    f, g, w = lib.moe_adamw_step, lib.moe_grad_norm, lib.moe_grad_norm_workspace_bytes
+    f, g, w, h = lib.moe_adamw_step, lib.moe_grad_norm, lib.moe_adamw_plan_bytes, lib.moe_adamw_plan
 
-    def step(t, count=1, state=32, lr=A, b1=0.9, b2=0.95, eps=1e-8, norm=NUL, most=0.0, at=A, ticket=A):
-        return f(t, count, state, lr, b1, b2, eps, norm, most, at, ticket, NUL)
+    def plan(t, count=1, p=A, size=BIG):
+        return h(t, count, p, size, NUL)
+
+    def step(t, count=1, p=A, size=BIG, lr=A, b1=0.9, b2=0.95, eps=1e-8, norm=NUL, most=0.0, at=A):
+        return f(t, count, p, size, lr, b1, b2, eps, norm, most, at, NUL)
     for kw, want in ((dict(n=-1), INVALID), (dict(n=(1 << 34) + 1), UNSUPPORTED), (dict(param_type=2), INVALID),
                      (dict(grad_type=-1), INVALID), (dict(reserved=1), INVALID), (dict(param=0), INVALID),
                      (dict(grad=0), INVALID), (dict(m=0), INVALID), (dict(v=0), INVALID), (dict(param=4104), MISALIGNED),
                      (dict(grad=4104), MISALIGNED), (dict(m=4104), MISALIGNED), (dict(v=4104), MISALIGNED),
-                     (dict(master=4104), MISALIGNED), (dict(m_scales=4096), INVALID),
+                     (dict(master=4104), MISALIGNED), (dict(m_scales=4096), INVALID), (dict(v_scales=4096), INVALID),
                      (dict(weight_decay=float("nan")), INVALID)):
-        assert step(table(**kw)) == want, kw
+        assert plan(table(**kw)) == want, kw
     t = table()
-    assert step(t, state=8) == INVALID and step(t, state=16) == INVALID            # no scales; no such state
+    two = (nat.AdamWTensor * 2)(t[0], table(m_scales=4097, v_scales=4099)[0])
+    assert plan(two, count=2) == INVALID                          # moments of two kinds
+    for call in (plan, step):
+        assert call(None, count=1) == INVALID and call(t, count=-1) == INVALID
+        assert call(t, p=NUL) == INVALID and call(t, p=MIS) == MISALIGNED
+        assert call(t, size=ctypes.c_size_t(w(t, 1) - 1)) == INVALID
     assert step(t, b1=1.0) == INVALID and step(t, b2=-0.1) == INVALID and step(t, eps=-1.0) == INVALID
     assert step(t, eps=float("inf")) == INVALID and step(t, b1=float("nan")) == INVALID
     assert step(t, norm=A, most=0.0) == INVALID and step(t, norm=A, most=float("nan")) == INVALID
-    assert step(t, lr=NUL) == INVALID and step(t, at=NUL) == INVALID and step(t, ticket=NUL) == INVALID
-    assert step(t, lr=ctypes.c_void_p(4098)) == MISALIGNED and step(None, count=1) == INVALID and step(t, count=-1) == INVALID
-    assert w(t, 1) >= 8 and w(t, -1) == 0 and w(table(n=-1), 1) == 0
+    assert step(t, lr=NUL) == INVALID and step(t, at=NUL) == INVALID
+    assert step(t, lr=ctypes.c_void_p(4098)) == MISALIGNED
+    assert w(t, 1) > 0 and w(t, -1) == 0 and w(table(n=-1), 1) == 0 and w(two, 2) == 0
+    many = (nat.AdamWTensor * 65)(*[table(n=1 << 34)[0]] * 65)
+    assert w(many, 64) > 0 and w(many, 65) == 0                   # 2^40 elements in all
     assert g(t, 1, NUL, BIG, A, NUL) == INVALID and g(t, 1, A, BIG, NUL, NUL) == INVALID
     assert g(t, 1, MIS, BIG, A, NUL) == MISALIGNED and g(t, 1, A, ctypes.c_size_t(4), A, NUL) == INVALID
-    assert g(table(grad=0), 1, A, BIG, A, NUL) == INVALID
+    assert g(t, 1, A, BIG, ctypes.c_void_p(4098), NUL) == MISALIGNED
 
 
 def test_moment_conversion_validation():

@@ -186,7 +186,7 @@ def test_steps(sizes, pt, masters, gt, state):
         opt.step_()
         torch.cuda.synchronize()
         check_step(opt, before, float(opt.lr.item()), t)
-        assert opt.step.item() == t and opt.ticket.item() == 0
+        assert opt.step.item() == t
 
 
 def test_the_first_step_without_clipping_and_with_a_decay_for_each():
@@ -207,7 +207,7 @@ def test_more_tensors_than_a_launch_takes(state):
         before = snapshot(opt)
         opt.step_()
         check_step(opt, before, float(opt.lr.item()), t)
-        assert opt.step.item() == t and opt.ticket.item() == 0
+        assert opt.step.item() == t
 
 
 def test_types_mixed_in_one_call():
@@ -229,7 +229,7 @@ def test_a_step_whose_norm_is_not_finite_is_not_taken(bad, state):
     opt.grads[1][20] = bad
     held = [t.clone() for t in opt.params + opt.masters + sum(opt.moments.values(), [])]
     opt.step_()
-    assert not math.isfinite(opt.norm.item()) and opt.step.item() == 11 and opt.ticket.item() == 0
+    assert not math.isfinite(opt.norm.item()) and opt.step.item() == 11
     assert all(torch.equal(a, b) for a, b in zip(held, opt.params + opt.masters + sum(opt.moments.values(), [])))
     opt.grads[1][20] = 1e-3
     before = snapshot(opt)
@@ -243,7 +243,7 @@ def test_gradients_whose_squares_leave_float32():
     for grads, want in (([big], 1e25 * math.sqrt(3000)), ([small], 1e-30 * math.sqrt(70))):
         p = [torch.zeros_like(g) for g in grads]
         opt = MoEAdamW(p, grads, lr=1e-3, max_norm=1.0)
-        moe_grad_norm(opt.table, opt.workspace, opt.norm)
+        moe_grad_norm(opt.table, opt.norm)
         assert abs(opt.norm.item() - want) <= 4 * U * want
     opt = MoEAdamW([torch.ones(3000, device=DEV)], [big], lr=1e-3, max_norm=1.0, weight_decay=0.0)
     opt.step_()                                  # clipped to a norm of 1: every element 1 / sqrt(3000)
@@ -260,7 +260,7 @@ def test_gradient_norm_at_many_sizes():
         for dt in (BF16, F32):
             x = rnd(n, g).to(dt)
             opt = MoEAdamW([torch.zeros(n, device=DEV)], [x], max_norm=1.0)
-            moe_grad_norm(opt.table, opt.workspace, opt.norm)
+            moe_grad_norm(opt.table, opt.norm)
             want = x.double().square().sum().sqrt().item()
             assert abs(opt.norm.item() - want) <= 2 * U * want, (n, dt)
 
@@ -347,7 +347,7 @@ def test_captured_and_replayed():
         g.replay()
         eager.step_()
         torch.cuda.synchronize()
-        assert opt.step.item() == eager.step.item() == 4 + i and opt.ticket.item() == 0
+        assert opt.step.item() == eager.step.item() == 4 + i
         for a, b in zip(opt.params + opt.masters + sum(opt.moments.values(), []),
                         eager.params + eager.masters + sum(eager.moments.values(), [])):
             assert torch.equal(a, b), i
@@ -409,4 +409,4 @@ def test_refusals():
     with pytest.raises(ValueError, match="scales"):
         MoEAdamW([z(8)], [z(8)], state="q8", moments=dict(m=[z(8)], v=[z(8)]))
     with pytest.raises(MoEError):                    # off by 4 bytes
-        MoEAdamW([z(12)[1:9]], [z(8)]).step_()
+        MoEAdamW([z(12)[1:9]], [z(8)])

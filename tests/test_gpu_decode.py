@@ -104,6 +104,12 @@ SIZES = [
     (2, 64, 16384, 5, 3),
     (40, 576, 576, 16, 3),
     (64, 960, 704, 128, 8),
+    (8, 128, 64, 64, 20),           # a wave a token, more picks than a row of lanes
+    (9, 128, 64, 64, 32),           # 16 lanes a token, all their picks
+    (9, 192, 64, 200, 31),
+    (3, 64, 128, 256, 32),
+    (2, 64, 64, 257, 32),
+    (64, 64, 64, 16, 16),
 ]
 
 

@@ -304,7 +304,7 @@ def test_refusals():
     y, mean, rstd = torch.empty_like(x), torch.empty(4, device=DEV), torch.empty(4, device=DEV)
     with pytest.raises(ValueError, match="together"):
         moe_layer_norm_fwd(x, w, b, EPS, y, mean, rstd, residual=x)
-    with pytest.raises(ValueError, match="weight must be"):
+    with pytest.raises(ValueError, match="weight must have"):
         moe_layer_norm_fwd(x, w[:32], b, EPS, y, mean, rstd)
     with pytest.raises(ValueError, match="contiguous"):
         moe_layer_norm_fwd(draw((4, 128), BF16, 1)[:, :64], w, b, EPS, y, mean, rstd)
