@@ -10,21 +10,28 @@
 //   * No route list in memory and no launches for it: every workgroup of the
 //     first kernel routes all tokens itself (the first one writes ids and
 //     probabilities out) and sorts the routes by expert in LDS, the second one
-//     sorts them again from the ids.
-//   * A wave streams rows of weights in 64-column steps through a ring of its
-//     own in LDS: LDS DMA loads, whole 128-byte lines, no barrier and no
-//     registers held by loads on their way.  The routes' rows of the other
-//     operand come the same way in the same step.
+//     sorts them again from the ids.  The probabilities are computed when the
+//     first weights are on their way.
+//   * A wave streams rows of weights, a line of 128 bytes of each at a time,
+//     through a ring of its own in LDS: LDS DMA loads, whole lines, no barrier
+//     and no registers held by loads on their way.  The routes' rows of the
+//     other operand come the same way in the same step.
 //   * The products are 16x16x32 bf16 MFMAs with 16 weight rows as the first
 //     operand and up to 16 routes as the second.
 //   * First kernel: a tile holds 8 gate rows and their 8 up rows, so that a
-//     layer has many of them; the waves of a workgroup share its contraction
-//     and add their parts in order.
-//   * Second kernel: a workgroup owns 16 columns of y for all tokens and walks
-//     all experts in use, its waves sharing (expert, step) pairs evenly; a wave
-//     adds an expert's products to its sums of those columns in LDS, and the
-//     waves' sums meet in order at the end.  No atomics.
+//     layer has many of them, and the SwiGLU is a lane exchange.
+//   * Second kernel: a team of waves owns 8 (or 4) columns of y for all tokens
+//     and walks all experts in use; a wave adds an expert's products to its sums
+//     of those columns in LDS, and the waves' sums meet in order at the end.  No
+//     atomics.
+//
+// A layer of 128 experts (8 a token, H 2048, I 768), three sets of weights in
+// turn: one token 19.5 us a call (FC1 10, FC2 6.5: 3 of each before the first
+// weights leave), 16 tokens 125 us (FC1 82, FC2 42: 6.2 TB/s over both), 64 tokens
+// 202 us; 8 tokens of 64 experts of 7168 x 2048 533-560 us (6.6-6.9 TB/s; a plain
+// read reaches 7.0).
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "gemm_common.h"
@@ -50,6 +57,7 @@ struct DecodeArgs {
     float* topk_probs;           // first
     uint16_t* out;               // first: act [N*K, I]; second: y [N, H]
     int N, E, K, Kdim, ncols, wrows;
+    int share;                   // waves that share an item or a tile: 1, 2, 4 or 8
     uint32_t per_token;          // ceil(2^16 / K): route r is token r * per_token >> 16, exact for r < 2048
     __device__ __forceinline__ int token(int route) const { return static_cast<int>(static_cast<uint32_t>(route) * per_token >> 16); }
 };
@@ -130,15 +138,15 @@ struct DecodeRing {
         return static_cast<uint32_t>(((lane_id() % 8) ^ (row / 2 % 8)) * 16);
     }
     // Issue a step, `at` bytes behind the first one; the place it goes to has been
-    // read.  What `w1` and `x1` name (a row's second line) is left out past its end.
-    template <class XLIVE>
-    __device__ __forceinline__ void issue(uint32_t at, bool w1, XLIVE x1) {
+    // read.  Lines that wlive(i) and xlive(i) deny (past a row's end) become zeros.
+    template <class WLIVE, class XLIVE>
+    __device__ __forceinline__ void issue(uint32_t at, WLIVE wlive, XLIVE xlive) {
         const uint32_t to = base + put * BYTES;
         wait_lds();
-        dma16<true>(wsrc, woff[0] + at, to);
-        dma16<true>(wsrc, w1 ? woff[1] + at : kOob, to + 1024);
 #pragma unroll
-        for (int i = 0; i < XL; ++i) dma16(xsrc, x1(i) ? xoff[i] + at : kOob, to + (2 + i) * 1024);
+        for (int i = 0; i < 2; ++i) dma16<true>(wsrc, wlive(i) ? woff[i] + at : kOob, to + i * 1024);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) dma16(xsrc, xlive(i) ? xoff[i] + at : kOob, to + (2 + i) * 1024);
         put = put + 1 == DEPTH ? 0 : put + 1;
     }
     // Multiply the oldest step, which has arrived once DEPTH - 1 are on their way.
@@ -301,24 +309,39 @@ __host__ __device__ constexpr int list_bytes(int E, int routes, int XR, bool pro
     return 16 + E * 4 + (probs ? routes * 4 : 0) + (routes < E + routes / XR ? routes : E + routes / XR) * 4 + routes * 2;
 }
 
-// ---------------------------------------------------------------- first kernel
-// A step is a line of the 8 gate rows and the 8 up rows of a tile, and of up to
-// 8*XL routes' tokens.  Workgroups take (block, tile) items in turn, tiles of one
-// block behind each other.  (A run of items for each, so that it reads front to
-// back, leaves the slowest one 9% behind: a wide layer's 2.5 GB 372 us, 347 in
-// turn.)
+// A workgroup's waves in teams of p.share.  Unit u of a kernel's work (an item, a
+// tile) is team u / G of workgroup u % G's, so that neighbouring workgroups are at
+// neighbouring weights and every compute unit has work when there is little.
+constexpr int kDecodeWaves = 8;
+struct Teams {
+    int size, member, first, stride;
+    __device__ __forceinline__ Teams(int share, int wave) {
+        size = share;
+        member = wave & (share - 1);
+        const int teams = kDecodeWaves / share, team = wave / share;
+        first = team * static_cast<int>(gridDim.x);     // past this workgroup's own number
+        stride = teams * static_cast<int>(gridDim.x);
+    }
+};
 
-constexpr int kFc1Waves = 8;
+// ---------------------------------------------------------------- first kernel
+// An item is a tile (8 gate rows and their 8 up rows) for a block of up to 8*XL
+// routes.  A team's waves share its contraction; the first one adds the others'
+// parts in order, while they go on with the next item.  A step is a line of the
+// 16 rows and of the routes' tokens; items begin at different lines of theirs,
+// since rows whose pitch is a large power of two put the same line of all rows on
+// few memory channels.
+
 template <int LANES, int PER, int XL, int DEPTH>
-__global__ __launch_bounds__(kFc1Waves * kWave) void decode_fc1_kernel(DecodeArgs p) {
+__global__ __launch_bounds__(kDecodeWaves * kWave) void decode_fc1_kernel(DecodeArgs p) {
     typedef DecodeRing<XL, DEPTH> Ring;
-    constexpr int W = kFc1Waves;
-    constexpr int XR = 8 * XL, CT = XL > 1 ? XL / 2 : 1, RING = W * DEPTH * Ring::BYTES, PARTS = W * CT * 1024;
+    constexpr int W = kDecodeWaves;
+    constexpr int XR = 8 * XL, CT = XL > 1 ? XL / 2 : 1, RING = W * DEPTH * Ring::BYTES, PARTS = 2 * W * CT * 1024;
     static_assert(RING + PARTS < kCuLds, "LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[kCuLds];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int routes = p.N * p.K;                       // <= 2048
-    floatx4* const parts = reinterpret_cast<floatx4*>(smem + RING);
+    floatx4* const parts = reinterpret_cast<floatx4*>(smem + RING);    // [2][W][CT][64]
     DecodeLists l;
     l.total = reinterpret_cast<int*>(smem + RING + PARTS);
     l.at = l.total + 4;
@@ -346,16 +369,19 @@ __global__ __launch_bounds__(kFc1Waves * kWave) void decode_fc1_kernel(DecodeArg
     }
 
     const int tiles = p.ncols / 8, items = *l.total * tiles;           // < 2^22
-    const int steps = p.Kdim / kLine, lo = steps * wave / W, hi = steps * (wave + 1) / W;
+    const Teams team(p.share, wave);
+    const int lines = p.Kdim / kLine, lo = lines * team.member / team.size, n = lines * (team.member + 1) / team.size - lo;   // n >= 1
     Ring ring;
     ring.init(smem + wave * DEPTH * Ring::BYTES);
     ring.xsrc = make_rsrc(p.a, static_cast<uint32_t>(p.N) * p.Kdim * 2u);
-    int item = lo < hi ? static_cast<int>(blockIdx.x) : items, k = lo;     // what is issued next
+    int item = team.first + static_cast<int>(blockIdx.x), k = 0, left = 0;   // what is issued next
     auto aim = [&]() {                                  // at the rows of `item`
         if (item >= items) {
             ring.close();
             return;
         }
+        k = item * 5 % n;
+        left = n;
         const uint32_t b = l.block[item / tiles];
         const int e = __builtin_amdgcn_readfirstlane(block_expert(b)), c0 = item % tiles * 8;
         const int64_t each = static_cast<int64_t>(p.wrows) * p.Kdim;
@@ -371,10 +397,11 @@ __global__ __launch_bounds__(kFc1Waves * kWave) void decode_fc1_kernel(DecodeArg
         }
     };
     auto issue = [&]() {
-        ring.issue(item < items ? k * 128 : 0, true, [](int) { return true; });
-        if (item < items && ++k == hi) {
-            k = lo;
-            item += gridDim.x;
+        ring.issue(item < items ? (lo + k) * 128 : 0, [](int) { return true; }, [](int) { return true; });
+        if (item >= items) return;
+        if (++k == n) k = 0;
+        if (--left == 0) {
+            item += team.stride;
             aim();
         }
     };
@@ -398,50 +425,76 @@ __global__ __launch_bounds__(kFc1Waves * kWave) void decode_fc1_kernel(DecodeArg
             if (blockIdx.x == 0) p.topk_probs[r] = prob;
         }
     }
+    meet();                                             // the probabilities are there
+    int turn = 0;
 #pragma unroll 1
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it0 = blockIdx.x; it0 < items; it0 += team.stride, turn ^= 1) {
+        const int it = it0 + team.first;
         floatx4 acc[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (it < items) {
 #pragma unroll 1
-        for (int s = lo; s < hi; ++s) {
-            issue();
-            ring.template multiply<CT>(acc, [&](int c) { return XL == 1 ? lane & 7 : c * 16 + (lane & 15); });
-        }
-        meet();                                         // the last item's parts are read
-#pragma unroll
-        for (int c = 0; c < CT; ++c) parts[(wave * CT + c) * kWave + lane] = acc[c];
-        meet();
-        const uint32_t b = l.block[it / tiles];
-        const int n = block_routes(b), c0 = it % tiles * 8;
-        for (int i = threadIdx.x; i < n * 8; i += W * kWave) {
-            const int j = i / 8, r = i % 8;
-            // gate row r of the tile is element r % 4 of lane (j % 16, r / 4), its up row 8 rows below
-            const float* at = reinterpret_cast<const float*>(parts + j / 16 * kWave + r / 4 * 16 + j % 16) + r % 4;
-            float g = 0.0f, u = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                g += at[w * CT * kWave * 4];
-                u += at[w * CT * kWave * 4 + 2 * 16 * 4];
+            for (int s = 0; s < n; ++s) {
+                issue();
+                ring.template multiply<CT>(acc, [&](int c) { return XL == 1 ? lane & 7 : c * 16 + (lane & 15); });
             }
-            const int route = l.route[block_first(b) + j];
-            p.out[static_cast<int64_t>(route) * p.ncols + c0 + r] = f32_to_bf16(silu(g) * u * probs[route]);
+        }
+        if (team.size > 1) {
+            floatx4* const mine = parts + (turn * W + wave) * CT * kWave + lane;
+            if (team.member > 0) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) mine[c * kWave] = acc[c];
+            }
+            // A buffer is written again two items on, past the next item's meeting,
+            // to which the first wave comes when it has read this one.
+            meet();
+            if (team.member > 0) continue;
+            for (int m = 1; m < team.size; ++m) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) acc[c] += mine[(m * CT + c) * kWave];
+            }
+        }
+        if (it >= items) continue;
+        // lane (j, q): gate rows 4q .. 4q+3 of route j for q < 2, the up rows beside them 32 lanes on
+        const uint32_t b = l.block[it / tiles];
+        const int c0 = it % tiles * 8;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            float u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(acc[c][i], 32);
+            const int j = c * 16 + (lane & 15);
+            if (lane < 32 && (lane & 15) < min(XR, 16) && j < block_routes(b)) {
+                const int route = l.route[block_first(b) + j];
+                const float pr = probs[route];
+                uint2 o;
+                o.x = pack_bf16x2(silu(acc[c][0]) * u[0] * pr, silu(acc[c][1]) * u[1] * pr);
+                o.y = pack_bf16x2(silu(acc[c][2]) * u[2] * pr, silu(acc[c][3]) * u[3] * pr);
+                *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(route) * p.ncols + c0 + (lane >> 4) * 4) = o;
+            }
         }
     }
     wait_vmcnt<0>();                                    // no load may land after the workgroup's LDS is given away
 }
 
 // ---------------------------------------------------------------- second kernel
-// A workgroup owns 8 columns of y.  A step is two lines of each of its 8 weight
-// rows, the second as rows 8-15 of the tile, and two lines of up to XR routes'
-// activations, the second as columns 8-15: of the 16x16 products the two 8x8
-// blocks on the diagonal are the two lines', the others mean nothing.  (Tiles of
-// 16 rows would be too few for the device: 128 of them in a layer of 2048
-// columns read 4.0 TB/s.)
+// A tile is R columns of y.  A step is 16/R lines of each of its R weight rows, line
+// after line as the 16 rows of the product, and the same lines of up to XR routes'
+// activations as its columns, R a line: of the 16x16 products the RxR blocks on the
+// diagonal are the lines', the others mean nothing.  (Tiles of 16 columns would be
+// too few for the device: 128 of them in a layer of 2048 columns read 4.0 TB/s.)
+// A team's waves share a tile's (block, step) pairs.
 
-template <int W, int XR, int DEPTH>
-__global__ __launch_bounds__(W * kWave) void decode_fc2_kernel(DecodeArgs p) {
-    constexpr int XL = XR / 4, CT = XR > 8 ? XR / 8 : 1;
+// 8-row loads of the routes' lines in a step, and its column tiles; with 8 rows and
+// 4 routes half the columns repeat the other half's.
+constexpr int fc2_loads(int R, int XR) { return XR * (16 / R) / 8; }
+constexpr int fc2_tiles(int R, int XR) { return XR > R ? XR / R : 1; }
+
+template <int R, int XR, int DEPTH>
+__global__ __launch_bounds__(kDecodeWaves * kWave) void decode_fc2_kernel(DecodeArgs p) {
+    constexpr int W = kDecodeWaves, XL = fc2_loads(R, XR), CT = fc2_tiles(R, XR), LINES = 16 / R;
+    constexpr int COLS = XR < R ? XR : R;               // columns of a line
     typedef DecodeRing<XL, DEPTH> Ring;
     constexpr int RING = W * DEPTH * Ring::BYTES;
     static_assert(RING < kCuLds, "LDS");
@@ -449,25 +502,29 @@ __global__ __launch_bounds__(W * kWave) void decode_fc2_kernel(DecodeArgs p) {
     const int lane = lane_id(), r16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int routes = p.N * p.K;
-    float* const sums = reinterpret_cast<float*>(smem + RING);         // [waves][N][8]
+    float* const sums = reinterpret_cast<float*>(smem + RING);         // [waves][N][R]
     DecodeLists l;
-    l.total = reinterpret_cast<int*>(sums + W * p.N * 8);
+    l.total = reinterpret_cast<int*>(sums + W * p.N * R);
     l.at = l.total + 4;
     l.block = reinterpret_cast<uint32_t*>(l.at + p.E);
     l.route = reinterpret_cast<uint16_t*>(l.block + min(routes, p.E + routes / XR));
     int* const ids = reinterpret_cast<int*>(smem);                     // in the ring's place
-
     const int live = p.n_live ? min(max(p.n_live[0], 0), p.N) : p.N;
-    // what the last lines add, loaded first: a thread has at most kDecodeMaxN * 8 / threads of them
-    constexpr int OUTS = (kDecodeMaxN * 8 + W * kWave - 1) / (W * kWave);
-    float out[OUTS];
+    const Teams team(p.share, wave);
+    // what a tile's last lines add is loaded first
+    constexpr int OUTS = kDecodeMaxN * R / kWave;
+    const int out0 = team.member * kWave + lane, outs = team.size * kWave;
+    const int tiles = p.ncols / R;
+    float added[OUTS];
+    auto load_added = [&](int tile) {
 #pragma unroll
-    for (int j = 0; j < OUTS; ++j) {
-        const int i = static_cast<int>(threadIdx.x) + j * W * kWave;
-        out[j] = p.residual && i < live * 8
-            ? bf16_to_f32(p.residual[static_cast<int64_t>(i / 8) * p.ncols + blockIdx.x * 8 + i % 8]) : 0.0f;
-    }
-    for (int i = threadIdx.x; i < W * p.N * 8; i += W * kWave) sums[i] = 0.0f;
+        for (int j = 0; j < OUTS; ++j) {
+            const int i = out0 + j * outs;
+            added[j] = p.residual && tile < tiles && i < live * R
+                ? bf16_to_f32(p.residual[static_cast<int64_t>(i / R) * p.ncols + tile * R + i % R]) : 0.0f;
+        }
+    };
+    load_added(team.first + static_cast<int>(blockIdx.x));
     if (p.N == 1) {
         if (wave == 0) {
             const int e = lane < p.K ? p.topk_ids[lane] : -1;          // device data: range-checked
@@ -489,18 +546,21 @@ __global__ __launch_bounds__(W * kWave) void decode_fc2_kernel(DecodeArgs p) {
         list_routes(l, ids, reinterpret_cast<uint16_t*>(ids + routes), routes);
     }
 
-    const int c0 = blockIdx.x * 8, lines = p.Kdim / kLine, steps = (lines + 1) / 2, pairs = *l.total * steps;
-    const int lo = static_cast<int>(static_cast<int64_t>(pairs) * wave / W);
-    const int hi = static_cast<int>(static_cast<int64_t>(pairs) * (wave + 1) / W);
+    const int lines = p.Kdim / kLine, steps = (lines + LINES - 1) / LINES, pairs = *l.total * steps;   // < 2^19
+    const int lo = pairs * team.member / team.size, hi = pairs * (team.member + 1) / team.size;
     Ring ring;
     ring.init(smem + wave * DEPTH * Ring::BYTES);
     ring.xsrc = make_rsrc(p.a, static_cast<uint32_t>(routes) * p.Kdim * 2u);
-    // the line and the route of the lane's row of load i: rows 0-7 of 16 are the first line's, of 8 rows 0-3
-    auto x_line = [&](int i) { return XR == 4 ? lane / 32 : i & 1; };
-    auto x_route = [&](int i) { return XR == 4 ? lane / 8 % 4 : i / 2 * 8 + lane / 8; };
-    int next = lo, block = lo / steps, k = lo % steps;                 // what is issued next
+    // the line, and the row or route, of the lane's row of load i
+    auto w_line = [&](int i) { return (i * 8 + lane / 8) / R; };
+    auto w_row = [&](int i) { return (i * 8 + lane / 8) % R; };
+    auto x_line = [&](int i) { return (i * 8 + lane / 8) % (COLS * LINES) / COLS; };
+    auto x_route = [&](int i) { return (i * 8 + lane / 8) / (COLS * LINES) * COLS + (i * 8 + lane / 8) % COLS; };
+    const int block0 = lo / steps, k0 = lo - block0 * steps;
+    int tile = lo < hi ? team.first + static_cast<int>(blockIdx.x) : tiles;
+    int next = lo, block = block0, k = k0;                             // what is issued next
     auto aim = [&]() {
-        if (next >= hi) {
+        if (tile >= tiles) {
             ring.close();
             return;
         }
@@ -510,7 +570,7 @@ __global__ __launch_bounds__(W * kWave) void decode_fc2_kernel(DecodeArgs p) {
         ring.wsrc = make_rsrc(p.w + e * each, static_cast<uint32_t>(each * 2));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            ring.woff[i] = static_cast<uint32_t>(c0 + lane / 8) * p.Kdim * 2u + i * 128 + Ring::piece(i * 8 + lane / 8);
+            ring.woff[i] = static_cast<uint32_t>(tile * R + w_row(i)) * p.Kdim * 2u + w_line(i) * 128 + Ring::piece(i * 8 + lane / 8);
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
             const int j = x_route(i);
@@ -520,62 +580,110 @@ __global__ __launch_bounds__(W * kWave) void decode_fc2_kernel(DecodeArgs p) {
         }
     };
     auto issue = [&]() {
-        const bool both = 2 * k + 1 < lines;
-        ring.issue(next < hi ? k * 256 : 0, both, [&](int i) { return both || x_line(i) == 0; });
-        if (next >= hi) return;
-        ++next;
-        if (++k == steps) {
+        const int rest = lines - k * LINES;             // lines from here on
+        ring.issue(tile < tiles ? k * (128 * LINES) : 0, [&](int i) { return w_line(i) < rest; },
+                   [&](int i) { return x_line(i) < rest; });
+        if (tile >= tiles) return;
+        ++k;
+        if (++next == hi) {
+            tile += team.stride;
+            next = lo;
+            block = block0;
+            k = k0;
+            aim();
+        } else if (k == steps) {
             k = 0;
             ++block;
+            aim();
         }
-        if (k == 0 || next == hi) aim();
     };
     aim();
 #pragma unroll 1
     for (int i = 0; i < DEPTH - 1; ++i) issue();
-    float* const mine = sums + wave * p.N * 8;
-    int at = lo;
+    float* const mine = sums + wave * p.N * R;
 #pragma unroll 1
-    while (at < hi) {
-        const int b = at / steps, end = min(hi, (b + 1) * steps);
-        floatx4 acc[CT];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t0 = blockIdx.x; t0 < tiles; t0 += team.stride) {
+        const int c0 = (t0 + team.first) * R;
+        const bool there = t0 + team.first < tiles;
+        for (int i = lane; i < p.N * R; i += kWave) mine[i] = 0.0f;
+        int at = there ? lo : hi, b = block0, end = min(hi, (block0 + 1) * steps);
 #pragma unroll 1
-        for (; at < end; ++at) {
-            issue();
-            ring.template multiply<CT>(acc, [&](int c) { return XR == 4 ? (r16 >> 3) * 4 + (r16 & 3) : c * 16 + r16; });
-        }
-        const uint32_t entry = l.block[b];
+        while (at < hi) {
+            floatx4 acc[CT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            floatx4 v;                                  // the second line's block is 8 rows and 8 columns on
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = acc[c][j] + __shfl_xor(acc[c][j], 40);
-            const int j = c * 8 + r16;
-            if (q < 2 && r16 < min(XR, 8) && j < block_routes(entry)) {   // a token has an expert once: lanes meet no one's sums
-                const int t = p.token(l.route[block_first(entry) + j]);
-                *reinterpret_cast<floatx4*>(mine + t * 8 + q * 4) += v;
+            for (int c = 0; c < CT; ++c) acc[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (; at < end; ++at) {
+                issue();
+                ring.template multiply<CT>(acc, [&](int c) { return c * 16 + (COLS < R ? r16 / R * COLS + r16 % COLS : r16); });
             }
+            const uint32_t entry = l.block[b];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                // The blocks of the diagonal: lane (q, r16) with r16 / R the line of its
+                // rows 4q .. 4q+3.  A line on is R rows and R columns on: xor 40 with
+                // two lines, 20 and 40 with four.
+                floatx4 v = acc[c];
+                if (R == 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], 20);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], 40);
+                const int j = c * COLS + r16;
+                if (q < R / 4 && r16 < COLS && j < block_routes(entry)) {     // a token has an expert once: lanes meet no one's sums
+                    const int t = p.token(l.route[block_first(entry) + j]);
+                    *reinterpret_cast<floatx4*>(mine + t * R + q * 4) += v;
+                }
+            }
+            ++b;
+            end = min(hi, end + steps);
+        }
+        if (team.size > 1) meet();
+        else wait_lds();
+        if (there) {
+#pragma unroll
+            for (int j = 0; j < OUTS; ++j) {
+                const int i = out0 + j * outs;
+                if (i >= live * R) break;
+                float v = 0.0f;
+                for (int m = 0; m < team.size; ++m) v += (mine - team.member * p.N * R)[m * p.N * R + i];
+                p.out[static_cast<int64_t>(i / R) * p.ncols + c0 + i % R] = f32_to_bf16(v + added[j]);
+            }
+        }
+        if (t0 + team.stride < tiles) {
+            load_added(t0 + team.stride + team.first);
+            if (team.size > 1) meet();                  // the sums are read
         }
     }
     wait_vmcnt<0>();
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < OUTS; ++j) {
-        const int i = static_cast<int>(threadIdx.x) + j * W * kWave;
-        if (i >= live * 8) break;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += sums[w * p.N * 8 + i];
-        p.out[static_cast<int64_t>(i / 8) * p.ncols + c0 + i % 8] = f32_to_bf16(v + out[j]);
+}
+
+// Waves that share a unit of work of `length` steps, of which there are `units`
+// (on average): as many as make the longest wave's time least.  A unit's end counts
+// as half a step, with several waves, who meet, as two.  (Always eight against this
+// rule: 2 tokens of 28 experts of 768 x 320 15.0 us against 13.9, 23 of 113 of 384 x
+// 896 33 against 30, 28 of 5 of 2496 x 192 18.3 against 16.8; large layers gain 1%
+// with eight: 16 tokens of 128 of 2048 x 768 124.9 against 125.9.)
+int decode_share(double units, int length) {
+    const int waves = device_cus() * kDecodeWaves;
+    int best = 1;
+    double least = 0.0;
+    for (int share = 1; share <= kDecodeWaves && share <= length; share *= 2) {
+        const double rounds = std::max(1.0, std::ceil(units * share / waves - 0.05));
+        const double time = rounds * ((length + share - 1) / share + (share > 1 ? 2.0 : 0.5));
+        if (share == 1 || time < least) {
+            least = time;
+            best = share;
+        }
     }
+    return best;
 }
 
 // Deep rings where the lists leave the room (LESS always does).
 template <int LANES, int PER, int XL, int DEEP, int LESS>
 void launch_fc1(const DecodeArgs& a, hipStream_t s) {
-    constexpr int W = kFc1Waves, XR = 8 * XL, PARTS = W * (XL > 1 ? XL / 2 : 1) * 1024;
+    constexpr int W = kDecodeWaves, XR = 8 * XL, PARTS = 2 * W * (XL > 1 ? XL / 2 : 1) * 1024;
     const int64_t most = std::min<int64_t>(a.N * a.K, a.E + a.N * a.K / XR) * (a.ncols / 8);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most, device_cus()));
     if (W * DEEP * DecodeRing<XL, DEEP>::BYTES + PARTS + list_bytes(a.E, a.N * a.K, XR, true) <= kCuLds)
@@ -591,14 +699,16 @@ void launch_fc1(const DecodeArgs& a, double mean, hipStream_t s) {
     else launch_fc1<LANES, PER, 4, 2, 2>(a, s);
 }
 
-template <int W, int XR, int DEEP, int LESS>
-void launch_fc2(const DecodeArgs& a, hipStream_t s) {
-    const int lists = list_bytes(a.E, a.N * a.K, XR, false) + W * a.N * 32;
-    const unsigned grid = static_cast<unsigned>(a.ncols / 8);
-    if (W * DEEP * DecodeRing<XR / 4, DEEP>::BYTES + lists <= kCuLds)
-        decode_fc2_kernel<W, XR, DEEP><<<grid, W * kWave, 0, s>>>(a);
+template <int R, int XR, int DEEP, int LESS>
+void launch_fc2(DecodeArgs a, double blocks, hipStream_t s) {
+    constexpr int W = kDecodeWaves, LINES = 16 / R;
+    const int lists = list_bytes(a.E, a.N * a.K, XR, false) + W * a.N * R * 4, tiles = a.ncols / R;
+    const unsigned grid = static_cast<unsigned>(std::min(tiles, device_cus()));
+    a.share = decode_share(tiles, std::max(1, static_cast<int>(blocks * ((a.Kdim / kLine + LINES - 1) / LINES))));
+    if (W * DEEP * DecodeRing<fc2_loads(R, XR), DEEP>::BYTES + lists <= kCuLds)
+        decode_fc2_kernel<R, XR, DEEP><<<grid, W * kWave, 0, s>>>(a);
     else
-        decode_fc2_kernel<W, XR, LESS><<<grid, W * kWave, 0, s>>>(a);
+        decode_fc2_kernel<R, XR, LESS><<<grid, W * kWave, 0, s>>>(a);
 }
 
 int check_decode(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K) {
@@ -638,7 +748,12 @@ extern "C" int moe_ffn_decode(const float* logits, const uint16_t* x, const uint
     a.out = static_cast<uint16_t*>(workspace);
     a.N = static_cast<int>(N); a.E = E; a.K = K; a.Kdim = H; a.ncols = I; a.wrows = 2 * I;
     a.per_token = (65536u + K - 1) / K;
-    const bool few = N <= kFc1Waves;
+    // experts that some token picks, on average, and blocks of up to XR of their routes
+    const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(K) / E, static_cast<double>(N)));
+    const int xr1 = mean <= 2 ? 8 : mean <= 8 ? 16 : 32, xr2 = mean <= 1 ? 4 : mean <= 3 ? 8 : 16;
+    const double blocks1 = used + N * K / (xr1 * 2.0) * (mean > 8), blocks2 = used + N * K / (xr2 * 2.0) * (mean > 8);
+    a.share = decode_share(blocks1 * (I / 8), H / kLine);
+    const bool few = N <= kDecodeWaves;
     if (E <= 16) launch_fc1<16, 1>(a, mean, stream);
     else if (E <= 64) few ? launch_fc1<64, 1>(a, mean, stream) : launch_fc1<16, 4>(a, mean, stream);
     else if (E <= 128) few ? launch_fc1<64, 2>(a, mean, stream) : launch_fc1<16, 8>(a, mean, stream);
@@ -646,8 +761,13 @@ extern "C" int moe_ffn_decode(const float* logits, const uint16_t* x, const uint
     else launch_fc1<64, 16>(a, mean, stream);
     a.a = static_cast<const uint16_t*>(workspace); a.w = w2; a.residual = residual; a.out = y;
     a.Kdim = I; a.ncols = H; a.wrows = H;
-    if (mean <= 1) launch_fc2<8, 4, 4, 4>(a, stream);
-    else if (mean <= 3) launch_fc2<8, 8, 4, 3>(a, stream);
-    else launch_fc2<8, 16, 2, 2>(a, stream);
+    // Tiles of 4 columns where those of 8 are few, up to 5 for 8 compute units (128 of
+    // them: 16 tokens of 64 experts of 1024 x 1024 65.7 us against 71, 48: 23 of 113 of
+    // 384 x 896 29.7 against 32.8; 192: 2 of 32 of 1536 x 1536 26.5 against 25.9, 232: 41
+    // of 26 of 1856 x 384 30.6 against 26.4).
+    const bool narrow = H / 8 * 8 < 5 * device_cus();
+    if (mean <= 1) narrow ? launch_fc2<4, 4, 4, 4>(a, blocks2, stream) : launch_fc2<8, 4, 4, 4>(a, blocks2, stream);
+    else if (mean <= 3) narrow ? launch_fc2<4, 8, 3, 2>(a, blocks2, stream) : launch_fc2<8, 8, 4, 3>(a, blocks2, stream);
+    else launch_fc2<8, 16, 2, 2>(a, blocks2, stream);
     return launch_status();
 }

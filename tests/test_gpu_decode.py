@@ -222,12 +222,9 @@ def test_weights_past_32_bit_offsets():
     logits = torch.zeros((2, E), device=DEV)
     logits[:, E - 1] = 3.0
     buf = DecodeBuffers(2, H, I, E, K)
-    got = forward_decode(buf, logits, x, w1, w2, residual=residual)
+    y = forward_decode(buf, logits, x, w1, w2, residual=residual)
     assert (buf.topk_ids == E - 1).all()
-    one = DecodeBuffers(2, H, I, 1, 1)
-    want = forward_decode(one, torch.zeros((2, 1), device=DEV), x, a, b, residual=residual)
-    check(one, torch.zeros((2, 1), device=DEV), x, a, b, residual, want)
-    assert torch.equal(got, want)
+    check(buf, logits, x, w1, w2, residual, y)       # (a layer of that expert alone shares its sums out otherwise)
 
 
 def test_captured_and_replayed():
