@@ -76,12 +76,20 @@ class BucketLadder:
 class ServingLadder:
     """Dropless MoE FFN forward for items of 1..max_tokens tokens, replayed
     from per-bucket graphs that share one set of static buffers.  w1 and w2
-    are bf16 tensors, or both W4Weights (4-bit expert weights)."""
+    are bf16 tensors, or both W4Weights (4-bit expert weights).
+
+    decode_tokens: items and buckets of up to this many tokens (at most
+    moe_ffn_decode_max_tokens(), bf16 weights) run as the two kernels of
+    moe_ffn_decode, whose sums round once, not once a route, so that their
+    results differ in the last bits from the grouped GEMMs'; 0: none do."""
 
     def __init__(self, w1, w2, K: int, expected: int, max_tokens: int, device="cuda",
                  max_padding_ratio: float = 1.25, reserve_bytes: int = 8 << 30,
-                 factors=DEFAULT_FACTORS, mem_get_info=None):
+                 factors=DEFAULT_FACTORS, mem_get_info=None, decode_tokens: int = 0):
         self.w4 = is_w4(w1, w2)
+        if decode_tokens and (self.w4 or not 0 < decode_tokens <= nat.moe_ffn_decode_max_tokens()):
+            raise ValueError(f"decode_tokens needs bf16 weights and 0..{nat.moe_ffn_decode_max_tokens()} tokens")
+        self.decode_tokens = min(int(decode_tokens), max_tokens)
         self.E, I2, self.H = w1.shape
         self.I = I2 // 2
         self.K = K
@@ -99,6 +107,9 @@ class ServingLadder:
         self.n_live = torch.zeros((1,), dtype=torch.int32, device=dev)
         from .forward import DroplessBuffers
         self.buf = DroplessBuffers(N, H, self.I, E, K, dev, w4=self.w4)
+        if self.decode_tokens:
+            self.decode_ws = torch.empty(
+                nat.moe_ffn_decode_workspace_bytes(self.decode_tokens, H, self.I, E, K), dtype=torch.uint8, device=dev)
         self.graphs = {}
         self.stream = torch.cuda.Stream(device=dev)
         self.counts = {"eager": 0}
@@ -107,6 +118,10 @@ class ServingLadder:
     def _forward(self, n: int, live: bool):
         b, K = self.buf, self.K
         lg = self.logits[:n]
+        if n <= self.decode_tokens:
+            nat.moe_ffn_decode(lg, self.x[:n], self.w1, self.w2, b.topk_ids[:n], b.topk_probs[:n], self.decode_ws,
+                               b.y[:n], n_live=self.n_live if live else None)
+            return
         if live:
             nat.moe_route_dropless_live(lg, K, self.n_live, b.topk_ids[:n], b.topk_probs[:n],
                                         b.route_within[:n], b.route_counts, b.sorted_slot_ids,
