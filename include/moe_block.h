@@ -59,7 +59,8 @@ size_t moe_ffn_decode_workspace_bytes(int64_t N, int32_t H, int32_t I, int32_t E
  *
  * Sums are float32 and rounded once; between the products only the activation
  * is rounded, as everywhere in the layer.  The same inputs give the same bits;
- * the order of a token's sum depends on which experts the batch uses.
+ * the order of a token's sums depends on the call's sizes and on which experts
+ * the batch uses, so a token's last bits can differ from one batch to another.
  * H, I multiples of 64 in [64, 16384], 1 <= K <= min(E, 32), E <= 1024. */
 int moe_ffn_decode(const float* logits, const uint16_t* x, const uint16_t* w1, const uint16_t* w2,
                    const uint16_t* residual, const int32_t* n_live, int64_t N, int32_t H, int32_t I,
@@ -108,7 +109,7 @@ size_t moe_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t D);
  *   dtotal   in  [rows, D] of x_type, the gradient that reaches h past the
  *                norm (through total); may be null
  *   dx       out [rows, D] of x_type: the gradient of x and of residual alike;
- *                may be dtotal, or dy if the types are equal
+ *                may be h or dtotal, or dy if the types are equal
  *   dweight  out float32 [D]; dbias out float32 [D], may be null
  *   accumulate   0: the weight gradients are written; 1: added to what is there
  *
@@ -160,13 +161,15 @@ typedef struct {
  * host, and the plan written for it: as long as the tensors stay where they
  * are, one plan serves every step.  Calls that share a plan must not overlap.
  * All tensors of a list have moments of the same kind; together at most 2^40
- * elements.  0 bytes: bad arguments. */
+ * elements.  No two of a list's buffers may overlap if a step writes one of them
+ * (gradients may).  0 bytes: bad arguments. */
 size_t moe_adamw_plan_bytes(const moe_adamw_tensor* tensors, int32_t count);
 int moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
                    hipStream_t stream);
 
-/* norm[0] = float32( sqrt( sum over all tensors of grad^2 ) ): squares and sums
- * in float64, in a fixed order. */
+/* norm[0] = float32( sqrt( sum over all tensors of grad^2 ) ): eight neighbours'
+ * squares in float32 (in float64 where their sum leaves 1e-25 .. 1e38), the sums
+ * of eight in float64, in a fixed order. */
 int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
                   float* norm, hipStream_t stream);
 
@@ -184,7 +187,7 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, si
  *   max_norm   > 0, used with grad_norm only
  *   step       in/out int32 [1], device scalar: steps taken so far; becomes t
  *
- * 0 <= beta < 1, eps >= 0.  No two tensors may share memory that is written. */
+ * 0 <= beta < 1, eps >= 0. */
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
                    const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
                    double max_norm, int32_t* step, hipStream_t stream);

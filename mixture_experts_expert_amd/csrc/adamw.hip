@@ -15,6 +15,8 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <utility>
+#include <vector>
 
 #include "gemm_common.h"
 #include "lowbit.h"
@@ -552,6 +554,36 @@ int check_list(const moe_adamw_tensor* t, int32_t count, ListShape* s) {
     return MOE_OK;
 }
 
+// Whether memory that a step writes belongs to two of its tensors, or holds a
+// gradient as well: workgroups would then change each other's elements.
+bool shares_memory(const moe_adamw_tensor* tensors, int32_t count) {
+    typedef std::pair<uintptr_t, uintptr_t> Range;
+    std::vector<Range> written, read;
+    for (int i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        const uintptr_t n = static_cast<uintptr_t>(t.n), groups = (n + kGroup - 1) / kGroup, state = t.m_scales ? 1 : 4;
+        auto add = [](std::vector<Range>& to, const void* p, uintptr_t bytes) {
+            if (p && bytes) to.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes);
+        };
+        add(written, t.param, n * (t.param_type == MOE_F32 ? 4 : 2));
+        add(written, t.master, n * 4);
+        add(written, t.m, n * state);
+        add(written, t.v, n * state);
+        add(written, t.m_scales, groups);
+        add(written, t.v_scales, groups);
+        add(read, t.grad, n * (t.grad_type == MOE_F32 ? 4 : 2));
+    }
+    std::sort(written.begin(), written.end());
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].first < written[i - 1].second) return true;
+    for (const Range& r : read) {                    // the first written range that ends behind its beginning
+        const auto at = std::upper_bound(written.begin(), written.end(), r.first,
+                                         [](uintptr_t a, const Range& w) { return a < w.second; });
+        if (at != written.end() && at->first < r.second) return true;
+    }
+    return false;
+}
+
 // The plan that goes with a list.
 int check_plan(const moe_adamw_tensor* t, int32_t count, const void* plan, size_t bytes, ListShape* s) {
     const int st = check_list(t, count, s);
@@ -581,6 +613,11 @@ extern "C" int moe_adamw_plan(const moe_adamw_tensor* tensors, int32_t count, vo
         if (t.n == 0) continue;
         if ((st = check_pointers({t.param, t.grad, t.m, t.v})) != MOE_OK) return st;
         if (!aligned16(t.master)) return MOE_ERR_MISALIGNED;
+    }
+    try {
+        if (shares_memory(tensors, count)) return MOE_ERR_INVALID_ARG;
+    } catch (...) {                                  // no host memory for a list of this length
+        return MOE_ERR_UNSUPPORTED;
     }
     const Plan p = Plan{static_cast<PlanHead*>(plan)};
     PlanBatch b{};

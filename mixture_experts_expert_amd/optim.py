@@ -3,7 +3,8 @@
 The gradients are buffers that the backward writes (a MoEBackwardBuffers'
 main_dw1 and main_dw2, a norm's dweight), so a step is two launches for any
 number of tensors, reads nothing back and can be captured into a hipGraph with
-the backward: the learning rate and the number of the step are device scalars.  All arithmetic runs in libmoe_native's kernels.
+the backward: the learning rate and the number of the step are device scalars.
+All arithmetic runs in libmoe_native's kernels.
 """
 
 from __future__ import annotations
@@ -31,6 +32,8 @@ class MoEAdamW:
     step         a number of steps taken, or an int32 [1] device tensor
 
     norm (float32 [1]) holds the last step's global norm, step the steps taken.
+    Parameters, gradients and state stay where they are from here on.  What is
+    made here is made on the current stream; no parameter may be given twice.
     """
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay=0.1,

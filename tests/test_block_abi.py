@@ -133,6 +133,19 @@ def test_adamw_validation():
     assert g(t, 1, A, BIG, ctypes.c_void_p(4098), NUL) == MISALIGNED
 
 
+def test_adamw_refuses_tensors_that_share_memory():
+    """Buffers of 64 elements 1 KB apart, but for one of a pair that begins inside another."""
+    def apart():
+        return [dict(n=64, param=base, master=base + 1024, grad=base + 2048, m=base + 3072, v=base + 4096, m_scales=0,
+                     v_scales=0, param_type=0, grad_type=1) for base in (1 << 20, 1 << 21)]
+    for a, b in ((("param", 0), ("param", 1)), (("param", 0), ("master", 0)), (("m", 0), ("v", 0)), (("m", 1), ("m", 0)),
+                 (("grad", 0), ("param", 1)), (("param", 1), ("grad", 0)), (("grad", 1), ("v", 1))):
+        t = apart()
+        t[a[1]][a[0]] = t[b[1]][b[0]] + 16                        # 16 bytes in, so that both overlap
+        two = (nat.AdamWTensor * 2)(*[table(**x)[0] for x in t])
+        assert lib.moe_adamw_plan(two, 2, A, BIG, NUL) == INVALID, (a, b)
+
+
 def test_moment_conversion_validation():
     for f, n_in in ((lib.moe_moment_values, 4), (lib.moe_moment_codes, 2)):
         n_out = 6 - n_in

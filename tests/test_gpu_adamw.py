@@ -408,5 +408,11 @@ def test_refusals():
         MoEAdamW([z(8)], [z(8)], weight_decay=[0.1, 0.2])
     with pytest.raises(ValueError, match="scales"):
         MoEAdamW([z(8)], [z(8)], state="q8", moments=dict(m=[z(8)], v=[z(8)]))
+    p = z(64)
+    for params, grads in (([p, p], [z(64), z(64)]), ([p, p[32:]], [z(64), z(32)]), ([p], [p])):
+        with pytest.raises(MoEError):                # a buffer that is written twice, or is a gradient too
+            MoEAdamW(params, grads)
+    g = z(64)
+    MoEAdamW([p[:32], p[32:]], [g[:32], g[:32]])     # neighbours, and a gradient for two
     with pytest.raises(MoEError):                    # off by 4 bytes
         MoEAdamW([z(12)[1:9]], [z(8)])

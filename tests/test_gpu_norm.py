@@ -17,8 +17,9 @@ backward, from the given mean and rstd: xhat is off by 3u of itself, so
 * c1, the mean of g xhat, by 70 u mean|g xhat|, c2 by 70 u mean|g|
 * dx: rstd (6u |g| + dc2 + 4u |c2| + |xhat| (dc1 + 8u |c1|)) + 4u (|dx| + |dtotal|)
   and the rounding
-* dweight, dbias: a lane adds its rows in turn (at most rows / (4 G) + 1 of
-  them), then 4 teams, G / 8 + 8 groups: (that + 8) u of the sum of magnitudes
+* dweight, dbias: a lane adds its rows in turn (one, or rows / 256 with 256
+  workgroups at work), then come up to 64 teams of a workgroup, 4 workgroups, 8 and
+  8 of their sums: (rows / 256 + 84 + 8) u of the sum of magnitudes
 """
 
 import pytest
@@ -100,7 +101,7 @@ def check_bwd(dy, h, w, mean, rstd, dx, dw, db, dtotal=None, old=None):
     bar = bar + 4 * U * want.abs()
     bar = bar + HALF[dx.dtype] * (want.abs() + bar)
     over = [((dx.double().reshape(rows, D) - want).abs() / bar.clamp(min=1e-300)).max().item() if rows else 0.0]
-    deep = rows / 4 + 100 if rows < 2048 else rows / 2048 + 100
+    deep = rows / 256 + 84
     for got, terms, k in ((dw, dy * xhat, 0), (db, dy, 1)):
         if got is None:
             continue
@@ -190,8 +191,8 @@ def test_gradients_against_differences(centre):
             assert abs(got.reshape(-1)[i].item() - want) <= 1e-4 * (1 + abs(want)), (k, i)
 
 
-def test_accumulated_weight_gradients_and_in_place_outputs():
-    rows, D = 300, 640
+@pytest.mark.parametrize("rows,D", [(300, 640), (40, 777), (9, 1111), (20, 5001), (5, 10001), (6, 5)])
+def test_accumulated_weight_gradients_and_in_place_outputs(rows, D):
     x, (w, b) = draw((rows, D), BF16, 31), params(D, 31)
     residual = draw((rows, D), BF16, 32)
     y, mean, rstd, total = run_fwd(x, w, b, BF16, True, residual)
@@ -207,6 +208,9 @@ def test_accumulated_weight_gradients_and_in_place_outputs():
     d3 = dy.clone()
     moe_layer_norm_bwd(d3, total, w, mean, rstd, d3, dw, db, ws, dtotal=dtotal)                 # in dy's
     assert torch.equal(d3, dx)
+    d4 = total.clone()
+    moe_layer_norm_bwd(dy, d4, w, mean, rstd, d4, dw, db, ws, dtotal=dtotal)                    # in h's
+    assert torch.equal(d4, dx)
     # the total in the place of x, and in the residual's; y in x's
     for place in (0, 1):
         a, r = x.clone(), residual.clone()
