@@ -9,9 +9,8 @@
 // Both are HBM-bound passes: a row is read once, kept in registers as float32
 // through its sums, and written once.  TL lanes share a row, V pieces of 8
 // columns each, so a lane holds at most 32 columns, and the weights of its
-// columns stay in registers from row to row.  Rows need not begin on a 16-byte
-// boundary (D is any number): pieces are loaded whole at any alignment, the
-// last one of a row by elements.
+// columns stay in registers from row to row.  Every load and store is of 16
+// aligned bytes whatever D is, but for a row's first and last columns.
 #include <algorithm>
 #include <initializer_list>
 
@@ -23,6 +22,8 @@ namespace {
 
 constexpr int kPiece = 8;            // columns a lane holds together
 constexpr int kNormThreads = 256;
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 struct Bf16 { uint16_t bits; };
 
@@ -47,6 +48,26 @@ struct Piece<Bf16> {
 #pragma unroll
         for (int j = 0; j < kPiece; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]);
     }
+    // The columns before lo and from hi on become 0.
+    __device__ __forceinline__ void keep(int lo, int hi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] &= (2 * i >= lo && 2 * i < hi ? 0xFFFFu : 0u) | (2 * i + 1 >= lo && 2 * i + 1 < hi ? 0xFFFF0000u : 0u);
+    }
+    // What was made of it is not known to be the same when it is made again.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("" : "+v"(w[i]));
+    }
+    // Column j + n comes to place j (n < 8), anything to the last n.
+    __device__ __forceinline__ void move_down(int n) {
+        if (n & 4) w[0] = w[2], w[1] = w[3];
+        if (n & 2) w[0] = w[1], w[1] = w[2], w[2] = w[3];
+        if (n & 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = w[i] >> 16 | (i < 3 ? w[i + 1] << 16 : 0u);
+        }
+    }
 };
 template <>
 struct Piece<float> {
@@ -57,52 +78,101 @@ struct Piece<float> {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) w[j] = v[j];
     }
-};
-
-// A lane's piece of a row: columns c .. c+7.  The last piece of a row whose D is
-// no multiple of 8 begins early, so that it can be loaded whole: its first
-// `skip` columns are another lane's, count as 0 and are not stored.  A lane
-// without a piece skips all 8.
-struct Place {
-    int c, skip;
-    __device__ __forceinline__ Place(int piece, int D) {
-        c = max(min(piece * kPiece, D - kPiece), 0);
-        skip = min(piece * kPiece - c, kPiece);
+    __device__ __forceinline__ void keep(int lo, int hi) {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) w[j] = j >= lo && j < hi ? w[j] : 0.0f;
+    }
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) asm("" : "+v"(w[j]));
+    }
+    __device__ __forceinline__ void move_down(int n) {
+#pragma unroll
+        for (int s = 4; s >= 1; s /= 2)
+            if (n & s) {
+#pragma unroll
+                for (int j = 0; j + s < kPiece; ++j) w[j] = w[j + s];
+            }
     }
 };
 
-// FEW: rows of under 8 columns, by elements.
-template <bool FEW, class T>
-__device__ __forceinline__ Piece<T> load8(const T* row, Place at, int D) {
+// A lane's piece of a row: columns c .. c+7, of which j = lo .. hi-1 are the
+// row's.  Where D is no multiple of 8 rows begin anywhere in 16 bytes of memory,
+// so a row's pieces begin `before` columns ahead of it, on 16 bytes: a first and
+// a last one are shared with its neighbours, whose columns are loaded, count as 0
+// and are not stored.  (Loaded where they fall, 2 bytes off: 8192 and more rows
+// in bf16 3.0 TB/s forward, 2.6 backward; so 4.6 and 4.1.)
+enum Width { kFew, kAny, kEights };      // under 8 columns; any more; a multiple of 8, all pieces whole
+
+template <int WIDTH>
+struct Place {
+    int c, lo, hi;
+    __device__ __forceinline__ Place(int piece, int before, int D) {
+        c = piece * kPiece - (WIDTH == kEights ? 0 : before);
+        lo = WIDTH == kEights ? 0 : max(-c, 0);
+        hi = WIDTH == kEights ? (c < D ? kPiece : 0) : min(max(D - c, 0), kPiece);
+    }
+    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == kPiece; }
+    __device__ __forceinline__ bool none() const { return hi == 0; }
+    __device__ __forceinline__ bool part() const { return WIDTH != kEights && !whole() && !none(); }
+    __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi; }
+};
+
+// The columns ahead of row r.  They are the same for every row a team works on,
+// since those are a multiple of 8 apart.
+__device__ __forceinline__ int columns_before(int64_t r, int D, int align) {
+    return static_cast<int>(r & 7) * (D & 7) & align;
+}
+
+// `last`: nothing may be read behind this row, whose last columns are then
+// loaded with those before them and moved down.
+template <int WIDTH, class T>
+__device__ __forceinline__ Piece<T> load8(const T* row, Place<WIDTH> at, bool last) {
     Piece<T> p{};
-    if (FEW) {
+    if (WIDTH == kFew) {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
-            if (at.skip == 0 && j < D) p.set(j, row[j]);
-        return p;
+            if (at.has(j)) p.set(j, row[at.c + j]);
+    } else if (!at.none()) {
+        const int over = WIDTH == kAny && last ? kPiece - at.hi : 0;
+        __builtin_memcpy(&p.w, row + at.c - over, kPiece * sizeof(T));
+        if (over) p.move_down(over);
     }
-    __builtin_memcpy(&p.w, row + at.c, kPiece * sizeof(T));
     return p;
 }
-template <bool FEW, class T>
-__device__ __forceinline__ void store8(T* row, Place at, int D, const float (&v)[kPiece]) {
-    if (!FEW && at.skip == 0) {
+// A vector of D, the same for all rows.
+template <int WIDTH>
+__device__ __forceinline__ void load_columns(const float* v, Place<WIDTH> at, float (&o)[kPiece]) {
+    Piece<float> p{};
+    if (at.whole()) {
+        __builtin_memcpy(&p.w, v + at.c, sizeof(p.w));
+    } else if (at.part()) {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j)
+            if (at.has(j)) p.set(j, v[at.c + j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) o[j] = p[j];
+}
+template <int WIDTH, class T>
+__device__ __forceinline__ void store8(T* row, Place<WIDTH> at, const float (&v)[kPiece]) {
+    if (at.whole()) {
         Piece<T> p;
         p.from(v);
         __builtin_memcpy(row + at.c, &p.w, kPiece * sizeof(T));
-    } else if (at.skip < kPiece) {
+    } else if (at.part()) {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
-            if (j >= at.skip && (!FEW || j < D)) narrow(v[j], &row[at.c + j]);
+            if (at.has(j)) narrow(v[j], &row[at.c + j]);
     }
 }
-// Another lane's columns become 0 (and those past the end of few).
-template <bool FEW>
-__device__ __forceinline__ void clear_skipped(float (&v)[kPiece], Place at, int D) {
-    if (FEW || at.skip > 0) {
+// Other rows' columns become 0 (a lane without a piece has zeros).
+template <int WIDTH>
+__device__ __forceinline__ void clear_others(float (&v)[kPiece], Place<WIDTH> at) {
+    if (at.part()) {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
-            if (j < at.skip || (FEW && j >= D)) v[j] = 0.0f;
+            if (!at.has(j)) v[j] = 0.0f;
     }
 }
 
@@ -130,10 +200,11 @@ struct NormArgs {
     float *mean, *rstd, *part;
     int64_t rows;
     int D, centre;
+    int align;                   // 7: pieces begin on 16 bytes, 0: on the row's first column
     float eps;
 };
 
-template <class TX, class TY, int TL, int V, bool FEW>
+template <class TX, class TY, int TL, int V, int WIDTH>
 __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fwd_kernel(NormArgs p) {
     constexpr int THREADS = TL > kNormThreads ? TL : kNormThreads;
     constexpr int ROWS = THREADS / TL;                   // rows of a workgroup at once
@@ -141,29 +212,30 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
     __shared__ float s_sum[2 * (TL / kWave > 0 ? TL / kWave : 1)];
     const int t = threadIdx.x % TL, D = p.D;
     const float inv = 1.0f / static_cast<float>(D);
+    const int64_t group = blockIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS, r0 = group * ROWS + threadIdx.x / TL;
+    const int before = columns_before(r0, D, p.align);
+    auto place = [&](int i) { return Place<WIDTH>(i * TL + t, before, D); };
     float w[V][kPiece], b[V][kPiece];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const Place at(i * TL + t, D);
-        const Piece<float> pw = load8<FEW>(p.weight, at, D);
-        Piece<float> pb{};
-        if (p.bias) pb = load8<FEW>(p.bias, at, D);
+        load_columns(p.weight, place(i), w[i]);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) w[i][j] = pw[j], b[i][j] = pb[j];
+        for (int j = 0; j < kPiece; ++j) b[i][j] = 0.0f;
+        if (p.bias) load_columns(p.bias, place(i), b[i]);
     }
-    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
     int turn = 0;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TL; r < p.rows; r += step) {
+    for (int64_t r = r0; r < p.rows; r += step) {
+        const bool last = r + 1 == p.rows;
         const TX* x = static_cast<const TX*>(p.x) + r * D;
         float h[V][kPiece];
         Piece<TX> in[V], add[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) in[i] = load8<FEW>(x, Place(i * TL + t, D), D);
+        for (int i = 0; i < V; ++i) in[i] = load8(x, place(i), last);
         if (p.residual) {
             const TX* res = static_cast<const TX*>(p.residual) + r * D;
 #pragma unroll
-            for (int i = 0; i < V; ++i) add[i] = load8<FEW>(res, Place(i * TL + t, D), D);
-            // (a lane's columns that are another's may be overwritten from here on: they are cleared)
+            for (int i = 0; i < V; ++i) add[i] = load8(res, place(i), last);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -172,7 +244,7 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
                     narrow(in[i][j] + add[i][j], &o);
                     h[i][j] = widen(o);
                 }
-                store8<FEW>(static_cast<TX*>(p.total) + r * D, Place(i * TL + t, D), D, h[i]);
+                store8(static_cast<TX*>(p.total) + r * D, place(i), h[i]);
             }
         } else {
 #pragma unroll
@@ -182,7 +254,7 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
         }
         float mean = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) clear_skipped<FEW>(h[i], Place(i * TL + t, D), D);
+        for (int i = 0; i < V; ++i) clear_others(h[i], place(i));
         if (p.centre) {
             float s = 0.0f;
 #pragma unroll
@@ -193,8 +265,8 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
 #pragma unroll
             for (int i = 0; i < V; ++i) {
 #pragma unroll
-                for (int j = 0; j < kPiece; ++j) h[i][j] -= mean;
-                clear_skipped<FEW>(h[i], Place(i * TL + t, D), D);
+                for (int j = 0; j < kPiece; ++j) h[i][j] -= place(i).none() ? 0.0f : mean;
+                clear_others(h[i], place(i));
             }
         }
         float s = 0.0f;
@@ -208,7 +280,7 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
         for (int i = 0; i < V; ++i) {
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) h[i][j] = h[i][j] * rstd * w[i][j] + b[i][j];
-            store8<FEW>(y, Place(i * TL + t, D), D, h[i]);
+            store8(y, place(i), h[i]);
         }
         if (t == 0) {
             if (p.mean) p.mean[r] = mean;
@@ -219,37 +291,53 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
 
 // The backward: dx of each row, and each workgroup's sums of the weights'
 // gradients over its rows, in `part` [2][G][D].  The next row is on its way
-// while one is worked on and the weights stay in registers, where there are
-// enough of them (not with 16 waves a workgroup).
+// while one is worked on, and a row is held as it is in memory and widened twice,
+// so that all of this stays in registers (not with float32 rows and 16 waves a
+// workgroup, where no row is loaded ahead).
 constexpr int kBwdThreads = 512;
 
-template <class TX, class TY, int TL, int V, bool FEW>
-__global__ __launch_bounds__(TL > kBwdThreads ? TL : kBwdThreads) void norm_bwd_kernel(NormArgs p) {
-    constexpr int ROWS = TL > kBwdThreads ? 1 : kBwdThreads / TL;
-    constexpr bool AHEAD = TL <= kBwdThreads;
+template <class TX, class TY, int TL, int V, int WIDTH>
+__global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
+    constexpr int ROWS = kBwdThreads / TL;
+    constexpr bool AHEAD = V <= 2 || sizeof(TX) == 2;
+    constexpr bool KEEP = V <= 2;
+    constexpr int PIECES = V * TL;
     __shared__ float s_sum[ROWS][2 * (TL / kWave > 0 ? TL / kWave : 1)];
-    __shared__ float s_part[ROWS > 1 ? ROWS - 1 : 1][ROWS > 1 ? V * TL * kPiece : 1];
+    __shared__ float s_part[ROWS][ROWS > 1 ? (PIECES + 1) * kPiece * (kWave + 1) / kWave + 1 : 1];
     const int t = threadIdx.x % TL, team = threadIdx.x / TL, D = p.D;
     const float inv = 1.0f / static_cast<float>(D);
-    float w[V][kPiece], dw[V][kPiece], db[V][kPiece];
+    const int64_t group = blockIdx.x;
+    int before = columns_before(group * ROWS + team, D, p.align);
+    auto place = [&](int i) { return Place<WIDTH>(i * TL + t, before, D); };
+    float w[V][kPiece], dw[KEEP ? V : 1][kPiece], db[KEEP ? V : 1][kPiece];
+    __shared__ floatx4 s_acc[KEEP ? 1 : 2 * V * 2][KEEP ? 1 : kBwdThreads];       // a lane's own, 16 bytes each: [half, piece, half a piece]
+    auto in_lds = [&](int half, int i, int j) -> float& { return reinterpret_cast<float*>(&s_acc[(half * V + i) * 2 + j / 4][t])[j % 4]; };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const Piece<float> pw = load8<FEW>(p.weight, Place(i * TL + t, D), D);
+        load_columns(p.weight, place(i), w[i]);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) w[i][j] = AHEAD ? pw[j] : 0.0f, dw[i][j] = db[i][j] = 0.0f;
+        for (int j = 0; j < kPiece; ++j) {
+            if (KEEP) dw[i][j] = db[i][j] = 0.0f;
+            else in_lds(0, i, j) = in_lds(1, i, j) = 0.0f;
+        }
     }
     struct Row {
         Piece<TX> h[V];
         Piece<TY> dy[V];
+        Piece<TX> dtotal[V];
         float mean, rstd;
     };
     auto load = [&](int64_t r) {
-        Row o{};
-        if (r >= p.rows) return o;                       // a team without a row keeps the others' barriers company
+        Row o;
+        if (ROWS > 1) r = min(r, p.rows - 1);                          // a team without a row keeps the others' barriers company
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            o.h[i] = load8<FEW>(static_cast<const TX*>(p.x) + r * D, Place(i * TL + t, D), D);
-            o.dy[i] = load8<FEW>(static_cast<const TY*>(p.dy) + r * D, Place(i * TL + t, D), D);
+            o.h[i] = load8(static_cast<const TX*>(p.x) + r * D, place(i), r + 1 == p.rows);
+            o.dy[i] = load8(static_cast<const TY*>(p.dy) + r * D, place(i), r + 1 == p.rows);
+        }
+        if (p.dtotal) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) o.dtotal[i] = load8(static_cast<const TX*>(p.dtotal) + r * D, place(i), r + 1 == p.rows);
         }
         o.mean = p.centre ? p.mean[r] : 0.0f;
         o.rstd = p.rstd[r];
@@ -258,70 +346,83 @@ __global__ __launch_bounds__(TL > kBwdThreads ? TL : kBwdThreads) void norm_bwd_
     const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
     int turn = 0;
     Row next{};
-    if (AHEAD) next = load(static_cast<int64_t>(blockIdx.x) * ROWS + team);
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS; r0 < p.rows; r0 += step) {
+    if (AHEAD) next = load(group * ROWS + team);
+    for (int64_t r0 = group * ROWS; r0 < p.rows; r0 += step) {
         const int64_t r = r0 + team;
-        const Row now = AHEAD ? next : load(r);
+        asm volatile("" : "+v"(before));                 // places are made anew: what depends on them takes 40 registers a piece
+        Row now = AHEAD ? next : load(r);
         if (AHEAD && r0 + step < p.rows) next = load(r + step);
-        float c1 = 0.0f, c2 = 0.0f, xh[V][kPiece], g[V][kPiece];
+        float c1 = 0.0f, c2 = 0.0f;
+        float xh[KEEP ? V : 1][kPiece], g[KEEP ? V : 1][kPiece];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) xh[i][j] = (now.h[i][j] - now.mean) * now.rstd, g[i][j] = now.dy[i][j];
-            clear_skipped<FEW>(xh[i], Place(i * TL + t, D), D);
-            clear_skipped<FEW>(g[i], Place(i * TL + t, D), D);
-            Piece<float> pw{};
-            if (!AHEAD) pw = load8<FEW>(p.weight, Place(i * TL + t, D), D);
+            const auto at = place(i);
+            const int k = KEEP ? i : 0;
+            if (at.part()) now.h[i].keep(at.lo, at.hi), now.dy[i].keep(at.lo, at.hi);
+            const bool mine = (ROWS == 1 || r < p.rows) && !at.none();
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
-                dw[i][j] += g[i][j] * xh[i][j];
-                db[i][j] += g[i][j];
-                g[i][j] *= AHEAD ? w[i][j] : pw[j];
-                c1 += g[i][j] * xh[i][j];
-                c2 += g[i][j];
+                xh[k][j] = (now.h[i][j] - now.mean) * now.rstd;
+                g[k][j] = mine ? now.dy[i][j] : 0.0f;
+                (KEEP ? dw[k][j] : in_lds(0, i, j)) += g[k][j] * xh[k][j];
+                (KEEP ? db[k][j] : in_lds(1, i, j)) += g[k][j];
+                g[k][j] *= w[i][j];
+                c1 += g[k][j] * xh[k][j];
+                c2 += g[k][j];
+            }
+            if (!KEEP) {
+                now.h[i].forget();
+                now.dy[i].forget();
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         c1 = row_total<TL>(c1, s_sum[team], turn++) * inv;
         c2 = p.centre ? row_total<TL>(c2, s_sum[team], turn++) * inv : 0.0f;
-        if (r >= p.rows) continue;
+        if (ROWS > 1 && r >= p.rows) continue;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const Place at(i * TL + t, D);
+            const auto at = place(i);
+            const int k = KEEP ? i : 0;
             float o[kPiece];
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) o[j] = (g[i][j] - c2 - xh[i][j] * c1) * now.rstd;
-            if (p.dtotal) {
-                const Piece<TX> a = load8<FEW>(static_cast<const TX*>(p.dtotal) + r * D, at, D);
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j) o[j] += a[j];
+            for (int j = 0; j < kPiece; ++j) {
+                if (!KEEP) xh[k][j] = (now.h[i][j] - now.mean) * now.rstd, g[k][j] = now.dy[i][j] * w[i][j];
+                o[j] = (g[k][j] - c2 - xh[k][j] * c1) * now.rstd;
             }
-            store8<FEW>(static_cast<TX*>(p.dx) + r * D, at, D, o);
+            if (p.dtotal) {
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) o[j] += now.dtotal[i][j];
+            }
+            store8(static_cast<TX*>(p.dx) + r * D, at, o);
+            if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // the teams of the workgroup add theirs in order
+    // The teams' sums of a column are added in order.  In LDS a column of 64 is
+    // left out after every 64, so that lanes eight columns apart meet no other's bank.
+    auto spot = [](int column) { return column + column / kWave; };
 #pragma unroll 1
     for (int half = 0; half < (p.bias ? 2 : 1); ++half) {
-        __syncthreads();
-        if (team > 0) {
+        float* part = p.part + (static_cast<int64_t>(half) * gridDim.x + group) * D;
+        if (ROWS > 1) {
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int j = 0; j < kPiece; ++j)
-                    s_part[ROWS > 1 ? team - 1 : 0][ROWS > 1 ? (i * kPiece + j) * TL + t : 0] = half ? db[i][j] : dw[i][j];
-        }
-        __syncthreads();
-        if (team == 0) {
-            float* part = p.part + (static_cast<int64_t>(half) * gridDim.x + blockIdx.x) * D;
+                for (int j = 0; j < kPiece; ++j) s_part[team][spot(place(i).c + kPiece + j)] = half ? db[KEEP ? i : 0][j] : dw[KEEP ? i : 0][j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < D; c += kBwdThreads) {
+                float s = 0.0f;
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k) s += s_part[k][spot(c + kPiece)];
+                part[c] = s;
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float o[kPiece];
 #pragma unroll
-                for (int j = 0; j < kPiece; ++j) o[j] = half ? db[i][j] : dw[i][j];
-#pragma unroll 1
-                for (int k = 0; k < ROWS - 1; ++k)
-#pragma unroll
-                    for (int j = 0; j < kPiece; ++j) o[j] += s_part[k][ROWS > 1 ? (i * kPiece + j) * TL + t : 0];
-                store8<FEW>(part, Place(i * TL + t, D), D, o);
+                for (int j = 0; j < kPiece; ++j) o[j] = KEEP ? (half ? db[KEEP ? i : 0][j] : dw[KEEP ? i : 0][j]) : in_lds(half, i, j);
+                store8(part, place(i), o);
             }
         }
     }
@@ -377,58 +478,73 @@ __global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(const float
 
 constexpr int kMaxNormDim = 16384;
 
-template <class TX, class TY, int TL, int V, bool FEW = false>
+template <class TX, class TY, int TL, int V, int WIDTH>
 void launch_fwd(const NormArgs& a, hipStream_t s) {
     constexpr int THREADS = std::max(TL, kNormThreads), ROWS = THREADS / TL;
     const int64_t blocks = std::min<int64_t>((a.rows + ROWS - 1) / ROWS, 2048);
-    norm_fwd_kernel<TX, TY, TL, V, FEW><<<static_cast<unsigned>(blocks), THREADS, 0, s>>>(a);
+    norm_fwd_kernel<TX, TY, TL, V, WIDTH><<<static_cast<unsigned>(blocks), THREADS, 0, s>>>(a);
 }
 
-// Lanes a row and pieces a lane for D columns.  The backward's sums take twice
-// the registers: at most two pieces a lane.
+// Pieces of a row of D columns, on 16 bytes: it begins up to 8 less its and 8's
+// common divisor behind one.  Rows too wide for one more begin at theirs.
+int pieces_on_16_bytes(int D) { return (D + (D % 8 ? 8 - (D & -D) : 0) + kPiece - 1) / kPiece; }
+int row_align(int D) { return D >= kPiece && pieces_on_16_bytes(D) <= kMaxNormDim / kPiece ? 7 : 0; }
+int row_pieces(int D) { return row_align(D) ? pieces_on_16_bytes(D) : (D + kPiece - 1) / kPiece; }
+
+// Lanes a row and pieces a lane.  The backward's sums take twice the registers:
+// at most two pieces a lane.
 constexpr int bwd_lanes(int pieces) {
     return pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 128 ? 64 : pieces <= 256 ? 128
-           : pieces <= 512 ? 256 : pieces <= 1024 ? 512 : 1024;
+           : pieces <= 512 ? 256 : 512;
+}
+template <class TX, class TY, int WIDTH>
+void by_pieces_fwd(const NormArgs& a, hipStream_t s) {
+    const int pieces = row_pieces(a.D);
+    if (pieces <= 8) launch_fwd<TX, TY, 8, 1, WIDTH>(a, s);
+    else if (pieces <= 16) launch_fwd<TX, TY, 16, 1, WIDTH>(a, s);
+    else if (pieces <= 32) launch_fwd<TX, TY, 32, 1, WIDTH>(a, s);
+    else if (pieces <= 64) launch_fwd<TX, TY, 64, 1, WIDTH>(a, s);
+    else if (pieces <= 128) launch_fwd<TX, TY, 64, 2, WIDTH>(a, s);
+    else if (pieces <= 256) launch_fwd<TX, TY, 64, 4, WIDTH>(a, s);
+    else if (pieces <= 512) launch_fwd<TX, TY, 256, 2, WIDTH>(a, s);
+    else if (pieces <= 1024) launch_fwd<TX, TY, 256, 4, WIDTH>(a, s);
+    else launch_fwd<TX, TY, 512, 4, WIDTH>(a, s);
 }
 template <class TX, class TY>
 void by_width_fwd(const NormArgs& a, hipStream_t s) {
-    const int pieces = (a.D + kPiece - 1) / kPiece;
-    if (a.D < kPiece) launch_fwd<TX, TY, 8, 1, true>(a, s);
-    else if (pieces <= 8) launch_fwd<TX, TY, 8, 1>(a, s);
-    else if (pieces <= 16) launch_fwd<TX, TY, 16, 1>(a, s);
-    else if (pieces <= 32) launch_fwd<TX, TY, 32, 1>(a, s);
-    else if (pieces <= 64) launch_fwd<TX, TY, 64, 1>(a, s);
-    else if (pieces <= 128) launch_fwd<TX, TY, 64, 2>(a, s);
-    else if (pieces <= 256) launch_fwd<TX, TY, 64, 4>(a, s);
-    else if (pieces <= 512) launch_fwd<TX, TY, 256, 2>(a, s);
-    else if (pieces <= 1024) launch_fwd<TX, TY, 256, 4>(a, s);
-    else launch_fwd<TX, TY, 512, 4>(a, s);
+    if (a.D < kPiece) launch_fwd<TX, TY, 8, 1, kFew>(a, s);
+    else if (a.D % kPiece) by_pieces_fwd<TX, TY, kAny>(a, s);
+    else by_pieces_fwd<TX, TY, kEights>(a, s);
+}
+template <class TX, class TY, int WIDTH>
+void by_pieces_bwd(const NormArgs& a, int G, hipStream_t s) {
+    const int pieces = row_pieces(a.D);
+    switch (bwd_lanes(pieces)) {
+        case 8: norm_bwd_kernel<TX, TY, 8, 1, WIDTH><<<G, kBwdThreads, 0, s>>>(a); return;
+        case 16: norm_bwd_kernel<TX, TY, 16, 1, WIDTH><<<G, kBwdThreads, 0, s>>>(a); return;
+        case 32: norm_bwd_kernel<TX, TY, 32, 1, WIDTH><<<G, kBwdThreads, 0, s>>>(a); return;
+        case 64:
+            if (pieces <= 64) norm_bwd_kernel<TX, TY, 64, 1, WIDTH><<<G, kBwdThreads, 0, s>>>(a);
+            else norm_bwd_kernel<TX, TY, 64, 2, WIDTH><<<G, kBwdThreads, 0, s>>>(a);
+            return;
+        case 128: norm_bwd_kernel<TX, TY, 128, 2, WIDTH><<<G, kBwdThreads, 0, s>>>(a); return;
+        case 256: norm_bwd_kernel<TX, TY, 256, 2, WIDTH><<<G, kBwdThreads, 0, s>>>(a); return;
+        default:
+            if (pieces <= 1024) norm_bwd_kernel<TX, TY, 512, 2, WIDTH><<<G, kBwdThreads, 0, s>>>(a);
+            else norm_bwd_kernel<TX, TY, 512, 4, WIDTH><<<G, kBwdThreads, 0, s>>>(a);
+    }
 }
 template <class TX, class TY>
 void by_width_bwd(const NormArgs& a, int G, hipStream_t s) {
-    const int pieces = (a.D + kPiece - 1) / kPiece;
-    switch (bwd_lanes(pieces)) {
-        case 8:
-            if (a.D < kPiece) norm_bwd_kernel<TX, TY, 8, 1, true><<<G, kBwdThreads, 0, s>>>(a);
-            else norm_bwd_kernel<TX, TY, 8, 1, false><<<G, kBwdThreads, 0, s>>>(a);
-            return;
-        case 16: norm_bwd_kernel<TX, TY, 16, 1, false><<<G, kBwdThreads, 0, s>>>(a); return;
-        case 32: norm_bwd_kernel<TX, TY, 32, 1, false><<<G, kBwdThreads, 0, s>>>(a); return;
-        case 64:
-            if (pieces <= 64) norm_bwd_kernel<TX, TY, 64, 1, false><<<G, kBwdThreads, 0, s>>>(a);
-            else norm_bwd_kernel<TX, TY, 64, 2, false><<<G, kBwdThreads, 0, s>>>(a);
-            return;
-        case 128: norm_bwd_kernel<TX, TY, 128, 2, false><<<G, kBwdThreads, 0, s>>>(a); return;
-        case 256: norm_bwd_kernel<TX, TY, 256, 2, false><<<G, kBwdThreads, 0, s>>>(a); return;
-        case 512: norm_bwd_kernel<TX, TY, 512, 2, false><<<G, kBwdThreads, 0, s>>>(a); return;
-        default: norm_bwd_kernel<TX, TY, 1024, 2, false><<<G, 1024, 0, s>>>(a);
-    }
+    if (a.D < kPiece) norm_bwd_kernel<TX, TY, 8, 1, kFew><<<G, kBwdThreads, 0, s>>>(a);
+    else if (a.D % kPiece) by_pieces_bwd<TX, TY, kAny>(a, G, s);
+    else by_pieces_bwd<TX, TY, kEights>(a, G, s);
 }
 
 // Workgroups of the backward: one a compute unit, since their sums, 8 * D bytes
 // each, are written and read once more, and no more than have a row.
 int bwd_groups(int64_t rows, int D) {
-    const int teams = std::max(1, kBwdThreads / bwd_lanes((D + kPiece - 1) / kPiece));
+    const int teams = kBwdThreads / bwd_lanes(row_pieces(D));
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>((rows + teams - 1) / teams, 1), 256));
 }
 
@@ -468,7 +584,7 @@ extern "C" int moe_layer_norm_fwd(const void* x, const void* residual, const flo
     if (y == total) return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.total = total; a.y = y;
-    a.mean = mean; a.rstd = rstd; a.rows = rows; a.D = D; a.centre = mean != nullptr;
+    a.mean = mean; a.rstd = rstd; a.rows = rows; a.D = D; a.centre = mean != nullptr; a.align = row_align(D);
     a.eps = static_cast<float>(eps);
     if (x_type == MOE_BF16) by_width_fwd<Bf16, Bf16>(a, stream);
     else if (y_type == MOE_BF16) by_width_fwd<float, Bf16>(a, stream);
@@ -498,6 +614,7 @@ extern "C" int moe_layer_norm_bwd(const void* dy, const void* h, const float* we
     a.x = h; a.dy = dy; a.dtotal = dtotal; a.weight = weight; a.bias = dbias; a.dx = dx;
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.part = static_cast<float*>(workspace); a.rows = rows; a.D = D; a.centre = mean != nullptr;
+    a.align = row_align(D);
     if (rows) {
         if (x_type == MOE_BF16) by_width_bwd<Bf16, Bf16>(a, G, stream);
         else if (y_type == MOE_BF16) by_width_bwd<float, Bf16>(a, G, stream);
