@@ -125,7 +125,8 @@ __device__ __forceinline__ int columns_before(int64_t r, int D, int align) {
 }
 
 // `last`: nothing may be read behind this row, whose last columns are then
-// loaded with those before them and moved down.
+// loaded with those before them, and moved down by `settle` before they are used
+// (not here: what follows a load would wait for it).
 template <int WIDTH, class T>
 __device__ __forceinline__ Piece<T> load8(const T* row, Place<WIDTH> at, bool last) {
     Piece<T> p{};
@@ -134,11 +135,17 @@ __device__ __forceinline__ Piece<T> load8(const T* row, Place<WIDTH> at, bool la
         for (int j = 0; j < kPiece; ++j)
             if (at.has(j)) p.set(j, row[at.c + j]);
     } else if (!at.none()) {
-        const int over = WIDTH == kAny && last ? kPiece - at.hi : 0;
-        __builtin_memcpy(&p.w, row + at.c - over, kPiece * sizeof(T));
-        if (over) p.move_down(over);
+        __builtin_memcpy(&p.w, row + at.c - (WIDTH == kAny && last ? kPiece - at.hi : 0), kPiece * sizeof(T));
     }
     return p;
+}
+// Other rows' columns become 0 (a lane without a piece has zeros).
+template <int WIDTH, class T>
+__device__ __forceinline__ void settle(Piece<T>& p, Place<WIDTH> at, bool last) {
+    if (WIDTH == kAny && at.part()) {
+        if (last && at.hi < kPiece) p.move_down(kPiece - at.hi);
+        p.keep(at.lo, at.hi);
+    }
 }
 // A vector of D, the same for all rows.
 template <int WIDTH>
@@ -160,16 +167,29 @@ __device__ __forceinline__ void store8(T* row, Place<WIDTH> at, const float (&v)
         Piece<T> p;
         p.from(v);
         __builtin_memcpy(row + at.c, &p.w, kPiece * sizeof(T));
-    } else if (at.part()) {
+    } else if (WIDTH == kFew) {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
             if (at.has(j)) narrow(v[j], &row[at.c + j]);
+    } else if (at.part()) {                              // 4, 2 and 1 of them, from the first on
+        Piece<T> p;
+        p.from(v);
+        T* to = row + at.c + at.lo;
+        p.move_down(at.lo);
+        const int n = at.hi - at.lo;
+#pragma unroll
+        for (int s = 4; s >= 1; s /= 2)
+            if (n & s) {
+                __builtin_memcpy(to, &p.w, s * sizeof(T));
+                p.move_down(s);
+                to += s;
+            }
     }
 }
-// Other rows' columns become 0 (a lane without a piece has zeros).
+// The same of values that have become others.
 template <int WIDTH>
 __device__ __forceinline__ void clear_others(float (&v)[kPiece], Place<WIDTH> at) {
-    if (at.part()) {
+    if (at.part() || at.none()) {
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
             if (!at.has(j)) v[j] = 0.0f;
@@ -238,6 +258,8 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
             for (int i = 0; i < V; ++i) add[i] = load8(res, place(i), last);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                settle(in[i], place(i), last);
+                settle(add[i], place(i), last);
 #pragma unroll
                 for (int j = 0; j < kPiece; ++j) {       // what is stored is what is normalised
                     TX o;
@@ -248,13 +270,13 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                settle(in[i], place(i), last);
 #pragma unroll
                 for (int j = 0; j < kPiece; ++j) h[i][j] = in[i][j];
+            }
         }
         float mean = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) clear_others(h[i], place(i));
         if (p.centre) {
             float s = 0.0f;
 #pragma unroll
@@ -265,7 +287,7 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
 #pragma unroll
             for (int i = 0; i < V; ++i) {
 #pragma unroll
-                for (int j = 0; j < kPiece; ++j) h[i][j] -= place(i).none() ? 0.0f : mean;
+                for (int j = 0; j < kPiece; ++j) h[i][j] -= mean;
                 clear_others(h[i], place(i));
             }
         }
@@ -358,7 +380,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
         for (int i = 0; i < V; ++i) {
             const auto at = place(i);
             const int k = KEEP ? i : 0;
-            if (at.part()) now.h[i].keep(at.lo, at.hi), now.dy[i].keep(at.lo, at.hi);
+            settle(now.h[i], at, r + 1 == p.rows);
+            settle(now.dy[i], at, r + 1 == p.rows);
             const bool mine = (ROWS == 1 || r < p.rows) && !at.none();
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
@@ -390,6 +413,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
                 o[j] = (g[k][j] - c2 - xh[k][j] * c1) * now.rstd;
             }
             if (p.dtotal) {
+                if (WIDTH == kAny && r + 1 == p.rows && at.part()) now.dtotal[i].move_down(kPiece - at.hi);
 #pragma unroll
                 for (int j = 0; j < kPiece; ++j) o[j] += now.dtotal[i][j];
             }
@@ -505,9 +529,12 @@ void by_pieces_fwd(const NormArgs& a, hipStream_t s) {
     else if (pieces <= 32) launch_fwd<TX, TY, 32, 1, WIDTH>(a, s);
     else if (pieces <= 64) launch_fwd<TX, TY, 64, 1, WIDTH>(a, s);
     else if (pieces <= 128) launch_fwd<TX, TY, 64, 2, WIDTH>(a, s);
+    else if (pieces <= 192) launch_fwd<TX, TY, 64, 3, WIDTH>(a, s);
     else if (pieces <= 256) launch_fwd<TX, TY, 64, 4, WIDTH>(a, s);
     else if (pieces <= 512) launch_fwd<TX, TY, 256, 2, WIDTH>(a, s);
+    else if (pieces <= 768) launch_fwd<TX, TY, 256, 3, WIDTH>(a, s);
     else if (pieces <= 1024) launch_fwd<TX, TY, 256, 4, WIDTH>(a, s);
+    else if (pieces <= 1536) launch_fwd<TX, TY, 512, 3, WIDTH>(a, s);
     else launch_fwd<TX, TY, 512, 4, WIDTH>(a, s);
 }
 template <class TX, class TY>
