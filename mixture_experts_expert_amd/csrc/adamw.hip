@@ -10,6 +10,11 @@
 // workgroup finds its work in two dependent loads.  (A table in the kernel's
 // arguments takes 44 tensors a launch and is read from host memory: 300 small
 // tensors 14 launches, 104 us.)
+//
+// Measured: 75.5 M elements with bf16 parameters, float32 master copies and
+// gradients: norm 41 to 55 us (5.5 to 7.4 TB/s; behind a step that has just written
+// everything, its reads compete with the write-back), step 390 with moments in 32
+// bits (6.2 TB/s), 221 in 8 (6.2); 300 tensors of 2.9 M elements in all: 6.7 + 14.
 #include <math.h>
 
 #include <algorithm>
