@@ -341,7 +341,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
     const int t = threadIdx.x % TL, team = threadIdx.x / TL, D = p.D;
     const float inv = 1.0f / static_cast<float>(D);
     const int64_t group = blockIdx.x;
-    int before = columns_before(group * ROWS + team, D, p.align);
+    // (a team without a row loads the last one, from its own first piece on)
+    int before = columns_before(min(group * ROWS + team, p.rows - 1), D, p.align);
     auto place = [&](int i) { return Place<WIDTH>(i * TL + t, before, D); };
     float w[V][kPiece], dw[KEEP ? V : 1][kPiece], db[KEEP ? V : 1][kPiece];
     __shared__ floatx4 s_acc[KEEP ? 1 : 2 * V * 2][KEEP ? 1 : kBwdThreads];       // a lane's own, 16 bytes each: [half, piece, half a piece]
@@ -363,7 +364,9 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
     };
     auto load = [&](int64_t r) {
         Row o;
-        if (ROWS > 1) r = min(r, p.rows - 1);                          // a team without a row keeps the others' barriers company
+        // A team without a row keeps the others' barriers company, with the last row: a
+        // branch around its loads costs 60 registers.
+        if (ROWS > 1) r = min(r, p.rows - 1);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             o.h[i] = load8(static_cast<const TX*>(p.x) + r * D, place(i), r + 1 == p.rows);
@@ -383,7 +386,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
     if (AHEAD) next = load(group * ROWS + team);
     for (int64_t r0 = group * ROWS; r0 < p.rows; r0 += step) {
         const int64_t r = r0 + team;
-        asm volatile("" : "+v"(before));                 // places are made anew: what depends on them takes 40 registers a piece
+        asm volatile("" : "+v"(before));                 // places are made anew: kept, what depends on them takes 10 registers a piece
         Row now = AHEAD ? next : load(r);
         if (AHEAD && r0 + step < p.rows) next = load(r + step);
         float c1 = 0.0f, c2 = 0.0f;

@@ -354,6 +354,23 @@ def test_captured_and_replayed():
         assert torch.equal(opt.norm, eager.norm)
 
 
+def test_two_graphs_that_share_a_plan_replayed_in_turn():
+    def build():
+        return make([9000, 4097, 5], "bf16", "f32", "f32", True, seed=12, lr=1e-3, max_norm=0.02)
+    opt, eager = build(), build()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            opt.step_()
+    for i in range(6):
+        graphs[i % 2].replay()
+        eager.step_()
+        torch.cuda.synchronize()
+        assert opt.step.item() == eager.step.item() and torch.equal(opt.norm, eager.norm)
+        assert all(torch.equal(a, b) for a, b in zip(opt.params + opt.masters, eager.params + eager.masters)), i
+
+
 def test_another_stream_and_nothing_beside_the_tensors():
     n, pad = 4099, 32
     bufs = [torch.full((n + 2 * pad,), 3.0, device=DEV) for _ in range(4)]

@@ -115,7 +115,10 @@ def check_bwd(dy, h, w, mean, rstd, dx, dw, db, dtotal=None, old=None):
 
 
 SHAPES = [(1, 1), (3, 7), (5, 64), (2, 512), (7, 513), (9, 1024), (4, 1111), (130, 2048), (3, 2049), (6, 4096),
-          (2, 5003), (11, 7168), (3, 8192), (2, 8193), (5, 16384), (2, 16383), (2500, 192), (700, 2048)]
+          (2, 5003), (11, 7168), (3, 8192), (2, 8193), (5, 16384), (2, 16383), (2500, 192), (700, 2048),
+          # rows that begin anywhere in 16 bytes, one and several of them to a team, each lanes-and-pieces form
+          (70000, 9), (20000, 13), (9000, 100), (5000, 250), (5000, 300), (3000, 513), (1, 777), (1500, 1111), (1030, 2047),
+          (700, 2049), (300, 4097), (260, 5002), (300, 8193), (300, 12292), (40, 16380)]
 TYPES = [(BF16, BF16), (F32, BF16), (F32, F32)]
 
 
@@ -250,6 +253,68 @@ def test_rows_far_from_zero_rows_of_one_value_and_rows_that_are_not_numbers(cent
     check_fwd(x[ok], w, b, y[ok], mean[ok] if centre else None, rstd[ok])
     assert torch.isnan(y[4]).all() and not torch.isfinite(y[3, 17])
     assert torch.isfinite(y[ok]).all()
+
+
+@pytest.mark.parametrize("rows,D", [(9, 9), (70, 33), (40, 515), (20, 1111), (11, 2049), (9, 8197), (5, 16383), (8, 5)])
+@pytest.mark.parametrize("tx,ty", TYPES)
+def test_rows_that_share_16_bytes_keep_to_themselves(rows, D, tx, ty):
+    """Every second row holds what is not a number: the others come out as without
+    them, bit for bit, and nothing before, behind or between is written twice."""
+    x, residual, dy, dtotal = (draw((rows, D), t, 91 + i) for i, t in enumerate((tx, tx, ty, tx)))
+    w, b = params(D, 91)
+    guard = 24                                             # elements: 16-byte aligned in either type
+
+    def between(t):
+        buf = torch.full((t.numel() + 2 * guard,), 7.25, dtype=t.dtype, device=DEV)
+        return buf, buf[guard:-guard].view(t.shape)
+
+    def run(x, dy):
+        keep, out = [], []
+        for like in (x, x.to(ty), x):
+            buf, view = between(like)
+            keep.append(buf), out.append(view)
+        total, y, dx = out
+        mean, rstd = torch.zeros(rows, device=DEV), torch.zeros(rows, device=DEV)
+        dw, db = torch.zeros(D, device=DEV), torch.zeros(D, device=DEV)
+        moe_layer_norm_fwd(x, w, b, EPS, y, mean, rstd, residual=residual, total=total)
+        moe_layer_norm_bwd(dy, total, w, mean, rstd, dx, dw, db, layer_norm_workspace(rows, D), dtotal=dtotal)
+        for buf in keep:
+            assert (buf[:guard] == 7.25).all() and (buf[-guard:] == 7.25).all()
+        return total, y, dx
+    clean = run(x, dy)
+    bad_x, bad_dy = x.clone(), dy.clone()
+    for i, v in enumerate((float("nan"), float("inf"), float("-inf"))):
+        bad_x[1 + 2 * i::6] = v
+        bad_dy[1 + 2 * i::6] = v
+    dirty = run(bad_x, bad_dy)
+    for c, d in zip(clean, dirty):
+        assert torch.equal(c[::2], d[::2])
+    assert torch.isnan(dirty[1][1]).all() and torch.isnan(dirty[2][1]).all()
+
+
+def test_two_streams_at_once():
+    cases = []
+    for i, (rows, D) in enumerate([(3000, 1111), (2000, 2048)]):
+        x, dy, (w, b) = draw((rows, D), BF16, 95 + i), draw((rows, D), BF16, 97 + i), params(D, 95 + i)
+        cases.append((x, dy, w, b, layer_norm_workspace(rows, D)))
+
+    def run(c, stream=None):
+        x, dy, w, b, ws = c
+        rows, D = x.shape
+        out = [torch.empty_like(x), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty_like(x),
+               torch.empty(D, device=DEV), torch.empty(D, device=DEV)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            moe_layer_norm_fwd(x, w, b, EPS, out[0], out[1], out[2], stream=stream)
+            moe_layer_norm_bwd(dy, x, w, out[1], out[2], out[3], out[4], out[5], ws, stream=stream)
+        return out
+    alone = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    both = [run(c, s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for a, t in zip(alone, both):
+        assert all(torch.equal(p, q) for p, q in zip(a, t))
 
 
 def test_rows_past_32_bit_offsets():
