@@ -227,11 +227,12 @@ struct NormArgs {
     const void *x, *residual, *dy, *dtotal;
     const float *weight, *bias;
     void *total, *y, *dx;
-    float *mean, *rstd, *part;
+    float *mean, *rstd, *part, *dweight, *dbias;
     int64_t rows;
     int D, centre;
     int align;                   // 7: pieces begin on 16 bytes, 0: on the row's first column
     float eps;
+    int accumulate;
 };
 
 template <class TX, class TY, int TL, int V, int WIDTH>
@@ -322,7 +323,8 @@ __global__ __launch_bounds__(TL > kNormThreads ? TL : kNormThreads) void norm_fw
 }
 
 // The backward: dx of each row, and each workgroup's sums of the weights'
-// gradients over its rows, in `part` [2][G][D].  The next row is on its way
+// gradients over its rows, in `part` [2][G][D] (the gradients themselves where
+// there is one workgroup).  The next row is on its way
 // while one is worked on: without its dtotal, loaded behind the row's sums, 2^25
 // bf16 elements of 2048 columns take 64 us instead of 54.  With four pieces a lane
 // (over 8192 columns) a row is held as it is in memory and widened twice, the
@@ -440,8 +442,9 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
     // left out after every 64, so that lanes eight columns apart meet no other's bank.
     auto spot = [](int column) { return column + column / kWave; };
 #pragma unroll 1
-    for (int half = 0; half < (p.bias ? 2 : 1); ++half) {
-        float* part = p.part + (static_cast<int64_t>(half) * gridDim.x + group) * D;
+    for (int half = 0; half < (p.dbias ? 2 : 1); ++half) {
+        const bool only = gridDim.x == 1;                // nothing else to add
+        float* part = only ? (half ? p.dbias : p.dweight) : p.part + (static_cast<int64_t>(half) * gridDim.x + group) * D;
         if (ROWS > 1) {
             __syncthreads();
 #pragma unroll
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
                 float s = 0.0f;
 #pragma unroll
                 for (int k = 0; k < ROWS; ++k) s += s_part[k][spot(c + kPiece)];
-                part[c] = s;
+                part[c] = only && p.accumulate ? part[c] + s : s;
             }
         } else {
 #pragma unroll
@@ -461,6 +464,12 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
                 float o[kPiece];
 #pragma unroll
                 for (int j = 0; j < kPiece; ++j) o[j] = KEEP ? (half ? db[KEEP ? i : 0][j] : dw[KEEP ? i : 0][j]) : in_lds(half, i, j);
+                if (only && p.accumulate) {
+                    float old[kPiece];
+                    load_columns(part, place(i), old);
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j) o[j] += old[j];
+                }
                 store8(part, place(i), o);
             }
         }
@@ -584,10 +593,14 @@ void by_width_bwd(const NormArgs& a, int G, hipStream_t s) {
 }
 
 // Workgroups of the backward: one a compute unit, since their sums, 8 * D bytes
-// each, are written and read once more, and no more than have a row.
+// each, are written and read once more, and no more than have a row.  A few rows
+// are one workgroup's, which writes the weights' gradients itself: up to four a
+// team (two where rows share 16 bytes, whose ends take longer), 7.8 to 9.3 us a call
+// against 10.2 with the second launch (eight: 14; four of 777 columns: 13).
 int bwd_groups(int64_t rows, int D) {
     const int teams = kBwdThreads / bwd_lanes(row_pieces(D));
-    return static_cast<int>(std::min<int64_t>(std::max<int64_t>((rows + teams - 1) / teams, 1), 256));
+    if (rows <= (D % kPiece ? 2 : 4) * teams) return 1;
+    return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, 256));
 }
 
 int check_norm(int64_t rows, int32_t D, int32_t x_type, int32_t y_type) {
@@ -653,7 +666,8 @@ extern "C" int moe_layer_norm_bwd(const void* dy, const void* h, const float* we
     const int G = bwd_groups(rows, D);
     if (workspace_bytes < moe_layer_norm_bwd_workspace_bytes(rows, D)) return MOE_ERR_INVALID_ARG;
     NormArgs a{};
-    a.x = h; a.dy = dy; a.dtotal = dtotal; a.weight = weight; a.bias = dbias; a.dx = dx;
+    a.x = h; a.dy = dy; a.dtotal = dtotal; a.weight = weight; a.dx = dx;
+    a.dweight = dweight; a.dbias = dbias; a.accumulate = accumulate;
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.part = static_cast<float*>(workspace); a.rows = rows; a.D = D; a.centre = mean != nullptr;
     a.align = row_align(D);
@@ -662,7 +676,7 @@ extern "C" int moe_layer_norm_bwd(const void* dy, const void* h, const float* we
         else if (y_type == MOE_BF16) by_width_bwd<float, Bf16>(a, G, stream);
         else by_width_bwd<float, float>(a, G, stream);
     }
-    norm_finish_kernel<<<dim3((D + kWave - 1) / kWave, dbias ? 2 : 1), kFinishThreads, 0, stream>>>(
+    if (!rows || G > 1) norm_finish_kernel<<<dim3((D + kWave - 1) / kWave, dbias ? 2 : 1), kFinishThreads, 0, stream>>>(
         a.part, rows ? G : 0, D, accumulate, dweight, dbias);
     return launch_status();
 }

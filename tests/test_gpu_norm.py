@@ -17,9 +17,10 @@ backward, from the given mean and rstd: xhat is off by 3u of itself, so
 * c1, the mean of g xhat, by 70 u mean|g xhat|, c2 by 70 u mean|g|
 * dx: rstd (6u |g| + dc2 + 4u |c2| + |xhat| (dc1 + 8u |c1|)) + 4u (|dx| + |dtotal|)
   and the rounding
-* dweight, dbias: a lane adds its rows in turn (one, or rows / 256 with 256
-  workgroups at work), then come up to 64 teams of a workgroup, 4 workgroups, 8 and
-  8 of their sums: (rows / 256 + 84 + 8) u of the sum of magnitudes
+* dweight, dbias: a lane adds its rows in turn (up to four of one workgroup's, one,
+  or rows / 256 with 256 workgroups at work), then come up to 64 teams of a
+  workgroup, 4 workgroups, 8 and 8 of their sums: (rows / 256 + 84 + 8) u of the sum
+  of magnitudes (one workgroup's: 4 + 64)
 """
 
 import pytest
@@ -118,7 +119,7 @@ SHAPES = [(1, 1), (3, 7), (5, 64), (2, 512), (7, 513), (9, 1024), (4, 1111), (13
           (2, 5003), (11, 7168), (3, 8192), (2, 8193), (5, 16384), (2, 16383), (2500, 192), (700, 2048),
           # rows that begin anywhere in 16 bytes, one and several of them to a team, each lanes-and-pieces form
           (70000, 9), (20000, 13), (9000, 100), (5000, 250), (5000, 300), (3000, 513), (1, 777), (1500, 1111), (1030, 2047),
-          (700, 2049), (300, 4097), (260, 5002), (300, 8193), (300, 12292), (40, 16380)]
+          (700, 2049), (300, 4097), (260, 5002), (16, 2048), (17, 2048), (256, 64), (9, 7168), (2, 4097), (3, 5003), (300, 8193), (300, 12292), (40, 16380)]
 TYPES = [(BF16, BF16), (F32, BF16), (F32, F32)]
 
 
@@ -194,7 +195,7 @@ def test_gradients_against_differences(centre):
             assert abs(got.reshape(-1)[i].item() - want) <= 1e-4 * (1 + abs(want)), (k, i)
 
 
-@pytest.mark.parametrize("rows,D", [(300, 640), (40, 777), (9, 1111), (20, 5001), (5, 10001), (6, 5)])
+@pytest.mark.parametrize("rows,D", [(300, 640), (40, 777), (9, 1111), (20, 5001), (5, 10001), (6, 5), (2, 4097), (4, 4104), (16, 1536)])
 def test_accumulated_weight_gradients_and_in_place_outputs(rows, D):
     x, (w, b) = draw((rows, D), BF16, 31), params(D, 31)
     residual = draw((rows, D), BF16, 32)
