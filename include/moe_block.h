@@ -36,7 +36,7 @@ extern "C" {
 int32_t moe_ffn_decode_max_tokens(void);
 
 /* Bytes of moe_ffn_decode's workspace: the activation between its kernels,
- * bf16 [N*K, I].  0 when the arguments fall outside the call's limits.
+ * bf16 [N*K, I], and the batch's routes by expert.  0 when the arguments fall outside the call's limits.
  * Host-only.  Contents between calls mean nothing; calls that share a
  * workspace must not overlap. */
 size_t moe_ffn_decode_workspace_bytes(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K);

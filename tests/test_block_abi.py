@@ -48,10 +48,10 @@ def test_decode_validation():
         assert call(at=i, ptr=MIS) == MISALIGNED, i
     assert call(y=NUL) == INVALID and call(y=MIS) == MISALIGNED and call(residual=MIS) == MISALIGNED
     assert call(n_live=ctypes.c_void_p(4098)) == MISALIGNED
-    assert call(size=ctypes.c_size_t(4 * 2 * 64 * 2 - 1)) == INVALID
+    assert call(size=ctypes.c_size_t(4 * 2 * 64 * 2 + 63)) == INVALID
     assert f(*[NUL] * 6, 0, 64, 64, 4, 2, NUL, NUL, NUL, 0, NUL, NUL) == OK
     g = lib.moe_ffn_decode_workspace_bytes
-    assert g(4, 64, 64, 4, 2) == 4 * 2 * 64 * 2 and g(65, 64, 64, 4, 2) == 0 and g(4, 65, 64, 4, 2) == 0
+    assert g(4, 64, 64, 4, 2) == 4 * 2 * 64 * 2 + 64 and g(65, 64, 64, 4, 2) == 0 and g(4, 65, 64, 4, 2) == 0
     with pytest.raises(moe.MoEError):
         moe.moe_ffn_decode_workspace_bytes(4, 64, 64, 2, 3)
 

@@ -21,7 +21,7 @@ import torch
 import moe_inputs
 from gpu_support import say
 from mixture_experts_expert_amd import (DecodeBuffers, DroplessBuffers, MoEError, ServingLadder, forward_decode,
-                                        forward_dropless, moe_ffn_decode, moe_ffn_decode_max_tokens)
+                                        forward_dropless, moe_ffn_decode, moe_ffn_decode_max_tokens, moe_ffn_decode_workspace_bytes)
 
 pytestmark = pytest.mark.gpu
 
@@ -284,7 +284,7 @@ def test_nothing_beside_the_outputs_is_written():
     ids, vids = band((N, K), torch.int32)
     probs, vprobs = band((N, K), torch.float32)
     y, vy = band((N, H), BF16)
-    need = N * K * I * 2
+    need = moe_ffn_decode_workspace_bytes(N, H, I, E, K)
     ws, vws = band((need,), torch.uint8)
     moe_ffn_decode(logits, x, w1, w2, vids, vprobs, vws, vy, residual=residual)
     torch.cuda.synchronize()
