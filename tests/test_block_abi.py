@@ -134,9 +134,9 @@ def test_adamw_validation():
 
 
 def test_adamw_refuses_tensors_that_share_memory():
-    """Buffers of 64 elements 1 KB apart, but for one of a pair that begins inside another."""
+    """Buffers of 64 elements 512 bytes apart, but for one of a pair that begins inside another."""
     def apart():
-        return [dict(n=64, param=base, master=base + 1024, grad=base + 2048, m=base + 3072, v=base + 4096, m_scales=0,
+        return [dict(n=64, param=base, master=base + 512, grad=base + 1024, m=base + 1536, v=base + 2048, m_scales=0,
                      v_scales=0, param_type=0, grad_type=1) for base in (1 << 20, 1 << 21)]
     for a, b in ((("param", 0), ("param", 1)), (("param", 0), ("master", 0)), (("m", 0), ("v", 0)), (("m", 1), ("m", 0)),
                  (("grad", 0), ("param", 1)), (("param", 1), ("grad", 0)), (("grad", 1), ("v", 1))):
