@@ -781,8 +781,9 @@ extern "C" int moe_ffn_decode(const float* logits, const uint16_t* x, const uint
     a.per_token = (65536u + K - 1) / K;
     // experts that some token picks, on average, and blocks of up to XR of their routes
     const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(K) / E, static_cast<double>(N)));
-    const int xr1 = mean <= 2 ? 8 : mean <= 8 ? 16 : 32, xr2 = mean <= 1 ? 4 : mean <= 3 ? 8 : 16;
-    const double blocks1 = used + N * K / (xr1 * 2.0) * (mean > 8), blocks2 = used + N * K / (xr2 * 2.0) * (mean > 8);
+    const bool narrow = H / 8 * 8 < 5 * device_cus(), slim = mean <= 8 && H / 4 <= device_cus();
+    const int xr1 = mean <= 2 ? 8 : mean <= 8 ? 16 : 32, xr2 = mean <= 1 ? 4 : mean <= 3 || slim ? 8 : 16;
+    const double blocks1 = used + N * K / (xr1 * 2.0) * (mean > 8), blocks2 = used + N * K / (xr2 * 2.0) * (mean > xr2 / 2);
     a.share = decode_share(blocks1 * (I / 8), H / kLine);
     a.lists = reinterpret_cast<int*>(static_cast<uint16_t*>(workspace) + N * K * I);
     a.next_log2 = xr2 == 4 ? 2 : xr2 == 8 ? 3 : 4;
@@ -798,9 +799,13 @@ extern "C" int moe_ffn_decode(const float* logits, const uint16_t* x, const uint
     // them: 16 tokens of 64 experts of 1024 x 1024 65.7 us against 71, 48: 23 of 113 of
     // 384 x 896 29.7 against 32.8; 192: 2 of 32 of 1536 x 1536 26.5 against 25.9, 232: 41
     // of 26 of 1856 x 384 30.6 against 26.4).
-    const bool narrow = H / 8 * 8 < 5 * device_cus();
+    // With more than 3 routes an expert, blocks of 8 for 4 columns instead of 16 for 8,
+    // where a compute unit has a tile at most and experts up to 8 routes (61 tokens of 61
+    // experts of 256 x 704, 6 each, 41.6 us against 48.7, 9 of 22 of 512 x 1088 28.3 against
+    // 32.9, 20 of 8 of 1024 x 1024 18.7 against 19.7; 27 routes of 1024 x 448 28.4 against 26.2,
+    // 11 of 960 x 576 20.1 against 18.3).
     if (mean <= 1) narrow ? launch_fc2<4, 4, 4, 4>(a, blocks2, stream) : launch_fc2<8, 4, 4, 4>(a, blocks2, stream);
     else if (mean <= 3) narrow ? launch_fc2<4, 8, 3, 2>(a, blocks2, stream) : launch_fc2<8, 8, 4, 3>(a, blocks2, stream);
-    else launch_fc2<8, 16, 2, 2>(a, blocks2, stream);
+    else slim ? launch_fc2<4, 8, 3, 2>(a, blocks2, stream) : launch_fc2<8, 16, 2, 2>(a, blocks2, stream);
     return launch_status();
 }

@@ -110,6 +110,10 @@ SIZES = [
     (3, 64, 128, 256, 32),
     (2, 64, 64, 257, 32),
     (64, 64, 64, 16, 16),
+    (61, 256, 704, 61, 6),          # up to 8 routes an expert on average, 4-column tiles
+    (9, 512, 1088, 22, 8),
+    (20, 1024, 192, 8, 2),
+    (20, 1088, 192, 8, 2),          # more tiles than compute units: 8 columns
 ]
 
 
