@@ -72,15 +72,16 @@ struct DecodeLists {
     int* at;                     // [E] counts, then each expert's next free route | its count << 16
     uint32_t* block;             // [blocks]
     uint16_t* route;             // [N*K] routes t*K + k, an expert's together
-    int* total;                  // blocks, and whether an expert has several
+    int* total;                  // blocks, and whether some expert's routes are to be in order
 };
 __device__ __forceinline__ int block_expert(uint32_t b) { return static_cast<int>(b & 1023u); }
 __device__ __forceinline__ int block_first(uint32_t b) { return static_cast<int>(b >> 10 & 4095u); }
 __device__ __forceinline__ int block_routes(uint32_t b) { return static_cast<int>(b >> 22); }
 
 // From the counts in `at` to blocks and each expert's first route (one wave).
+// `whole`: the routes of an expert that no block divides, here or further on.
 template <int XR>
-__device__ __forceinline__ void list_blocks(const DecodeLists& l, int E, int lane) {
+__device__ __forceinline__ void list_blocks(const DecodeLists& l, int E, int whole, int lane) {
     int routes = 0, blocks = 0, split = 0;
     for (int e0 = 0; e0 < E; e0 += kWave) {
         const int e = e0 + lane, n = e < E ? l.at[e] : 0, nb = (n + XR - 1) / XR;
@@ -94,7 +95,7 @@ __device__ __forceinline__ void list_blocks(const DecodeLists& l, int E, int lan
         const int last = __builtin_amdgcn_readlane(inc, kWave - 1);
         routes += last & 0xFFFF;
         blocks += last >> 16;
-        split |= __ballot(nb > 1) != 0;
+        split |= __ballot(n > whole) != 0;
     }
     if (lane == 0) {
         l.total[0] = blocks;
@@ -284,10 +285,12 @@ __device__ __forceinline__ void list_one(const DecodeLists& l, int e, int lane) 
     if (lane == 0) *l.total = __popcll(there);
 }
 
-// The routes of each expert together, by the whole workgroup.  The order among
-// an expert's routes moves no result as long as they are one block (each is a
-// column of its own); of several blocks every workgroup has to have the same,
-// and then the routes are put in order.  `spare`: [N*K].
+// The routes of each expert together, by the whole workgroup, as they come.  The
+// order among an expert's routes moves no result as long as they are one block
+// (each is a column of its own).  Where some expert has several, the block decides
+// which waves sum a route, so that the same inputs give the same bits only in one
+// order, ascending: in every workgroup for the first kernel's blocks, and in the
+// one that hands its lists on for the second one's, which are smaller.  `spare`: [N*K].
 __device__ __forceinline__ void list_routes(const DecodeLists& l, const int* ids, uint16_t* spare, int routes) {
     const bool split = l.total[1] != 0;
     uint16_t* const to = split ? spare : l.route;
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(kDecodeWaves * kWave) void decode_fc1_kernel(Decode
     float* const probs = reinterpret_cast<float*>(l.at + p.E);
     l.block = reinterpret_cast<uint32_t*>(probs + routes);
     l.route = reinterpret_cast<uint16_t*>(l.block + min(routes, p.E + routes / XR));
-    const bool one = p.N == 1;
+    const bool one = p.N == 1, hands_on = !one && blockIdx.x == gridDim.x - 1;
     int* const ids = one ? l.at : reinterpret_cast<int*>(smem);        // (in the ring's place, which is not in use yet)
     const int live = p.n_live ? min(max(p.n_live[0], 0), p.N) : p.N;
 
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(kDecodeWaves * kWave) void decode_fc1_kernel(Decode
         __syncthreads();
         decode_route<LANES, PER, W>(p, live, l.at, ids, probs);
         __syncthreads();
-        if (wave == 0) list_blocks<XR>(l, p.E, lane);
+        if (wave == 0) list_blocks<XR>(l, p.E, hands_on ? min(XR, 1 << p.next_log2) : XR, lane);
         __syncthreads();
         list_routes(l, ids, reinterpret_cast<uint16_t*>(ids + routes), routes);
     }
@@ -450,7 +453,7 @@ __global__ __launch_bounds__(kDecodeWaves * kWave) void decode_fc1_kernel(Decode
     aim();
 #pragma unroll 1
     for (int i = 0; i < DEPTH - 1; ++i) issue();
-    if (!one && blockIdx.x == gridDim.x - 1) hand_on(l, p, routes, wave, lane);    // (it has no more items than the others)
+    if (hands_on) hand_on(l, p, routes, wave, lane);    // (it has no more items than the others)
     // with the first loads on their way, probabilities from the logits: a wave takes
     // as many tokens as have their picks in its lanes, added in pick order
     const int fit = kWave / p.K;
