@@ -180,6 +180,9 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, si
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / ( sqrt(v) / sqrt(1 - beta2^t) + eps )
  * in float32, each result rounded once (8-bit moments: p moves by the moments
  * before they are rounded).
+ * 8-bit moments are rounded to the nearest code, which loses moves of less than half
+ * a code: right for a step or a few, but over a training run the moments do not
+ * follow the gradients (moe_moments.h has figures, and the step for that).
  *
  *   lr         in  float32 [1], device scalar
  *   grad_norm  in  float32 [1], device scalar (moe_grad_norm's); may be null.

@@ -1,5 +1,5 @@
 """ctypes binding of libmoe_native (the C ABI in include/moe_native.h,
-include/moe_lowbit.h and include/moe_block.h).
+include/moe_lowbit.h, include/moe_block.h and include/moe_moments.h).
 
 Argument marshalling only: every function takes torch tensors for the
 device buffers, checks dtype/device/contiguity/size on the host, passes raw
@@ -23,6 +23,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_native.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_native.h")
 LOWBIT_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_lowbit.h")
 BLOCK_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_block.h")
+MOMENTS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_moments.h")
 PROBE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe_probe.h")
 
 if not os.path.exists(LIB_PATH):
@@ -115,6 +116,8 @@ _SIGNATURES = {
     "moe_adamw_plan": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp]),
     "moe_grad_norm": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp, _vp]),
     "moe_adamw_step": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp, _f64, _f64, _f64, _vp, _f64, _vp, _vp]),
+    "moe_adamw_step_stochastic": (ctypes.c_int, [_vp, _i32, _vp, ctypes.c_size_t, _vp, _f64, _f64, _f64, _vp, _f64, _vp,
+                                                 ctypes.c_uint32, _vp]),
     "moe_moment_values": (ctypes.c_int, [_vp] * 4 + [_i64] + [_vp] * 3),
     "moe_moment_codes": (ctypes.c_int, [_vp] * 2 + [_i64] + [_vp] * 5),
     "moe_probe_read": (ctypes.c_int, [_vp, ctypes.c_size_t, _vp, _vp]),
@@ -1123,13 +1126,28 @@ def moe_grad_norm(table: AdamWTable, norm, stream=None):
 def moe_adamw_step(table: AdamWTable, lr, betas, eps: float, step, grad_norm=None, max_norm: float = 0.0,
                    stream=None):
     """One AdamW step of the table's tensors.  lr float32 [1], step int32 [1] (moved on) and grad_norm
-    float32 [1] (or None) are device scalars."""
+    float32 [1] (or None) are device scalars.  8-bit moments are rounded to nearest, and over many steps
+    do not follow the gradients: moe_adamw_step_stochastic's do."""
+    *args, st = _step_args(table, lr, betas, eps, step, grad_norm, max_norm, stream)
+    _check("moe_adamw_step", lib.moe_adamw_step(*args, st))
+
+
+def moe_adamw_step_stochastic(table: AdamWTable, lr, betas, eps: float, step, seed: int, grad_norm=None,
+                              max_norm: float = 0.0, stream=None):
+    """The step of a table with 8-bit moments, rounded stochastically by a hash of seed (0 to 2^32 - 1), step
+    and place."""
+    if not 0 <= seed < 1 << 32:
+        raise ValueError("seed must be 0 to 2^32 - 1")
+    *args, st = _step_args(table, lr, betas, eps, step, grad_norm, max_norm, stream)
+    _check("moe_adamw_step_stochastic", lib.moe_adamw_step_stochastic(*args, seed, st))
+
+
+def _step_args(table, lr, betas, eps, step, grad_norm, max_norm, stream):
     dev, st = table.here(stream)
     f32 = torch.float32
-    _check("moe_adamw_step", lib.moe_adamw_step(
-        table.address, table.count, table.plan_at, table.bytes, _at(lr, f32, 1, "lr", dev), betas[0], betas[1], eps,
-        0 if grad_norm is None else _at(grad_norm, f32, 1, "grad_norm", dev), max_norm,
-        _at(step, torch.int32, 1, "step", dev), st))
+    return (table.address, table.count, table.plan_at, table.bytes, _at(lr, f32, 1, "lr", dev), betas[0], betas[1], eps,
+            0 if grad_norm is None else _at(grad_norm, f32, 1, "grad_norm", dev), max_norm,
+            _at(step, torch.int32, 1, "step", dev), st)
 
 
 def moe_moment_values(m, m_scales, v, v_scales, m_values, root_values, stream=None):

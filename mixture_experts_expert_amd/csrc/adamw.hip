@@ -25,7 +25,7 @@
 
 #include "gemm_common.h"
 #include "lowbit.h"
-#include "../../include/moe_block.h"
+#include "../../include/moe_moments.h"
 
 namespace moe {
 namespace {
@@ -251,6 +251,11 @@ __device__ __forceinline__ Eight first_values(u32x2 w, uint32_t b) {
     return v;
 }
 
+// Both scales without room for rounding past the largest code: a magnitude above
+// 448, 1.9375 for a root, goes to the next.
+__device__ __forceinline__ int first_scale_above(uint32_t amax) { return scale_byte<0x1FFFFFu, 8>(amax); }
+__device__ __forceinline__ int root_scale_above(uint32_t amax) { return scale_byte<0x7FFFFu, 0>(amax); }
+
 // Unsigned e4m4 without subnormals: the exponent and the upper four bits of the
 // mantissa of a float in [2^-15, 2), counted from 2^-15 on; code 0 is 0.
 __device__ __forceinline__ int root_scale(uint32_t amax) { return scale_byte<0x40000u, 0>(amax); }
@@ -274,6 +279,64 @@ __device__ __forceinline__ Eight root_values(u32x2 w, uint32_t b) {
         v[j] = (c ? __uint_as_float((c << 19) + (112u << 23)) : 0.0f) * s;
     }
     return v;
+}
+
+// Stochastic rounding.  32 random bits serve both moments: the upper 20 the first
+// one, the lower 24 the root, each of which decides by its own upper bits but once
+// in 256 times (their decisions' correlation is 0.004).  A bijection whose results'
+// bits all depend on all of x; the constants are 2^32 times the fractions of the
+// roots of 2 and 3 and of the golden ratio.
+constexpr uint32_t kGolden = 0x9E3779B9u;
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x ^ x >> 16;
+}
+__device__ __forceinline__ uint32_t chunk_key(uint32_t seed, uint32_t t, uint32_t chunk) {
+    return mix(mix(seed + kGolden * t) + chunk);
+}
+
+// e4m3 keeps 20 bits less of the mantissa, from 2^-6 on; below, 2^-6 is added, which
+// brings the values to where the codes are as far apart.  Random bits are added to
+// the bits that go, and carry with the probability of what those are worth.
+__device__ __forceinline__ float first_random(float a, uint32_t h) {
+    const float m = __builtin_fabsf(a), shift = m < 0x1p-6f ? 0x1p-6f : 0.0f;
+    const uint32_t bits = (__float_as_uint(m + shift) + (h >> 12)) & 0xFFF00000u;
+    return __builtin_copysignf(__uint_as_float(bits) - shift, a);
+}
+__device__ __forceinline__ u32x2 first_codes_random(const Eight& v, int b, uint32_t key, int at) {
+    const float inv = inv_scale(b);
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) r[j] = first_random(v[j] * inv, mix(key + kGolden * static_cast<uint32_t>(at + j)));
+    u32x2 o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                        // exact: they are codes' values
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(r[4 * i], r[4 * i + 1], 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(r[4 * i + 2], r[4 * i + 3], w, true);
+        o[i] = b == kScaleNaN ? 0u : static_cast<uint32_t>(w);
+    }
+    return o;
+}
+// The root's code below and the one above, which is taken where the random fraction
+// of the way between their squares has not reached the root's square.
+__device__ __forceinline__ u32x2 root_codes_random(const Eight& r, int b, uint32_t key, int at) {
+    const float inv = inv_scale(b);
+    u32x2 o = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const uint32_t h = mix(key + kGolden * static_cast<uint32_t>(at + j)) & 0xFFFFFFu;
+        const float x = r[j] * inv;
+        const uint32_t below = __float_as_uint(x) & 0xFFF80000u;
+        const float lo = __uint_as_float(below), hi = __uint_as_float(below + 0x80000u);
+        const bool up = static_cast<float>(h) * 0x1p-24f * ((hi - lo) * (hi + lo)) < (x - lo) * (x + lo);
+        const int c = static_cast<int>(below >> 19) - 112 * 16;
+        // a root below code 1 becomes that
+        o[j / 4] |= (r[j] > 0.0f ? static_cast<uint32_t>(c < 1 ? 1 : c + up) : 0u) << (8 * (j % 4));
+    }
+    return b == kScaleNaN ? u32x2{0u, 0u} : o;
 }
 
 // The hardware's root (1 ulp), which takes no subnormals: those are scaled up first.
@@ -394,6 +457,7 @@ struct AdamWArgs {
     int32_t* step;
     double log2_beta1, log2_beta2;                   // -inf for beta 0
     float beta1, beta2, one_less_beta1, one_less_beta2, eps, max_norm;
+    uint32_t seed;                                   // of stochastic rounding
     int chunk0, chunks;                              // this launch's first chunk, all launches' chunks
 };
 
@@ -412,9 +476,13 @@ struct AdamWScalars {
     }
 };
 
+// How moments are held: in 32 bits, or in 8, rounded to nearest or at random.
+enum State { kFloats, kNearest, kRandom };
+
 // A workgroup a chunk: all its loads are issued before the scalars are looked at.
-template <bool Q8>
+template <State STATE>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
+    constexpr bool Q8 = STATE != kFloats;
     const int c = b.chunk0 + static_cast<int>(blockIdx.x);
     const bool there = c < b.chunks;                 // (without any element one workgroup moves the step alone)
     const Chunk& e = b.plan.chunk()[there ? c : 0];
@@ -455,6 +523,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
         s.keep = 1.0f - lr * e.weight_decay;
         s.rate = static_cast<float>(lr / bc1);
         s.inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
+        const uint32_t key = STATE == kRandom ? chunk_key(b.seed, static_cast<uint32_t>(t), static_cast<uint32_t>(c)) : 0u;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int at = (i * kThreads + static_cast<int>(threadIdx.x)) * kEach;
@@ -468,9 +537,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
             s.update(g[i], m[i], v[i], root, p[i]);
             if (Q8) {
                 // elements past the end are zeros and take no part in the scale
-                const int bm = first_scale(group_max(m[i])), br = root_scale(group_max(root));
-                store8(static_cast<uint8_t*>(e.m), at, n, first_codes(m[i], bm));
-                store8(static_cast<uint8_t*>(e.v), at, n, root_codes(root, br));
+                const uint32_t am = group_max(m[i]), ar = group_max(root);
+                const int bm = STATE == kRandom ? first_scale_above(am) : first_scale(am);
+                const int br = STATE == kRandom ? root_scale_above(ar) : root_scale(ar);
+                store8(static_cast<uint8_t*>(e.m), at, n, STATE == kRandom ? first_codes_random(m[i], bm, key, at) : first_codes(m[i], bm));
+                store8(static_cast<uint8_t*>(e.v), at, n, STATE == kRandom ? root_codes_random(root, br, key, at) : root_codes(root, br));
                 if (at < n && at % kGroup == 0) {
                     e.m_scales[at / kGroup] = static_cast<uint8_t>(bm);
                     e.v_scales[at / kGroup] = static_cast<uint8_t>(br);
@@ -658,17 +729,20 @@ extern "C" int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, voi
     return launch_status();
 }
 
-extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
-                              const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
-                              double max_norm, int32_t* step, hipStream_t stream) {
-    using namespace moe;
+namespace moe {
+namespace {
+
+// `random`: 8-bit moments are rounded stochastically, with `seed`.
+int adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes, const float* lr, double beta1,
+               double beta2, double eps, const float* grad_norm, double max_norm, int32_t* step, bool random, uint32_t seed,
+               hipStream_t stream) {
     ListShape s;
     const int st = check_plan(tensors, count, plan, plan_bytes, &s);
     if (st != MOE_OK) return st;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
         (grad_norm && !(max_norm > 0.0)))
         return MOE_ERR_INVALID_ARG;
-    if (!lr || !step) return MOE_ERR_INVALID_ARG;
+    if (!lr || !step || (random && s.entries > 0 && s.state != 8)) return MOE_ERR_INVALID_ARG;
     if (!aligned4(lr) || !aligned4(step) || !aligned4(grad_norm)) return MOE_ERR_MISALIGNED;
     AdamWArgs a;
     a.plan = Plan{static_cast<PlanHead*>(plan)};
@@ -678,16 +752,33 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, vo
     a.one_less_beta1 = static_cast<float>(1.0 - beta1); a.one_less_beta2 = static_cast<float>(1.0 - beta2);
     a.eps = static_cast<float>(eps);
     a.max_norm = grad_norm ? static_cast<float>(max_norm) : 0.0f;
+    a.seed = seed;
     a.chunks = static_cast<int>(s.chunks);
     int64_t at = 0;
     do {
         const unsigned grid = static_cast<unsigned>(std::min(std::max<int64_t>(s.chunks - at, 1), kMaxBlocks));
         a.chunk0 = static_cast<int>(at);
-        if (s.state == 8) adamw_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-        else adamw_kernel<false><<<grid, kThreads, 0, stream>>>(a);
+        if (s.state != 8) adamw_kernel<kFloats><<<grid, kThreads, 0, stream>>>(a);
+        else if (random) adamw_kernel<kRandom><<<grid, kThreads, 0, stream>>>(a);
+        else adamw_kernel<kNearest><<<grid, kThreads, 0, stream>>>(a);
         at += grid;
     } while (at < s.chunks);
     return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                              const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
+                              double max_norm, int32_t* step, hipStream_t stream) {
+    return moe::adamw_step(tensors, count, plan, plan_bytes, lr, beta1, beta2, eps, grad_norm, max_norm, step, false, 0u, stream);
+}
+
+extern "C" int moe_adamw_step_stochastic(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
+                                         const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
+                                         double max_norm, int32_t* step, uint32_t seed, hipStream_t stream) {
+    return moe::adamw_step(tensors, count, plan, plan_bytes, lr, beta1, beta2, eps, grad_norm, max_norm, step, true, seed, stream);
 }
 
 namespace moe {
