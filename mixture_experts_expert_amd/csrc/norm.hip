@@ -391,6 +391,14 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
         asm volatile("" : "+v"(before));                 // places are made anew: kept, what depends on them takes 10 registers a piece
         Row now = AHEAD ? next : load(r);
         if (AHEAD && r0 + step < p.rows) next = load(r + step);
+        if (ROWS > 1 && r >= p.rows) {                   // no row: an infinity in the last one is not this team's to count
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                now.h[i] = Piece<TX>{};
+                now.dy[i] = Piece<TY>{};
+            }
+            now.mean = now.rstd = 0.0f;
+        }
         float c1 = 0.0f, c2 = 0.0f;
         float xh[KEEP ? V : 1][kPiece], g[KEEP ? V : 1][kPiece];
 #pragma unroll
@@ -399,11 +407,10 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs p) {
             const int k = KEEP ? i : 0;
             settle(now.h[i], at, r + 1 == p.rows);
             settle(now.dy[i], at, r + 1 == p.rows);
-            const bool mine = (ROWS == 1 || r < p.rows) && !at.none();
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
                 xh[k][j] = (now.h[i][j] - now.mean) * now.rstd;
-                g[k][j] = mine ? now.dy[i][j] : 0.0f;
+                g[k][j] = now.dy[i][j];
                 (KEEP ? dw[k][j] : in_lds(0, i, j)) += g[k][j] * xh[k][j];
                 (KEEP ? db[k][j] : in_lds(1, i, j)) += g[k][j];
                 g[k][j] *= w[i][j];
