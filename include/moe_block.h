@@ -85,8 +85,10 @@ typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
  *   total        out h, [rows, D] of x_type: given if and only if residual is;
  *                    may be x or residual
  *   y            out [rows, D] of y_type (x bf16: bf16; x float32: either);
- *                    may be x if the types are equal and total is not x
+ *                    may be x or residual if the types are equal and total is not it
  *   mean, rstd   out float32 [rows]; mean may be null (RMS norm)
+ *
+ * Outputs that share memory with another buffer in any other way are refused.
  *
  * 1 <= D <= 16384, any rows * D < 2^40; rows == 0: no-op.  Sums are float32;
  * the variance is the second pass's, over the row in registers. */
@@ -112,6 +114,9 @@ size_t moe_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t D);
  *                may be h or dtotal, or dy if the types are equal
  *   dweight  out float32 [D]; dbias out float32 [D], may be null
  *   accumulate   0: the weight gradients are written; 1: added to what is there
+ *
+ * Outputs (workspace_bytes as asked for among them) that share memory with another
+ * buffer in any other way are refused.
  *
  * Sums are float32, rows in a fixed order, no atomics: the same bits from the
  * same inputs.  Limits as the forward; rows == 0 writes zero weight gradients

@@ -629,6 +629,25 @@ int check_given(std::initializer_list<const void*> needed, std::initializer_list
     return MOE_OK;
 }
 
+// A buffer of a call.  What is written may share memory with nothing else of the
+// call, or, row by row, be one of the buffers that are named: a row is stored while
+// others are still to be read.
+struct Span {
+    const void* at;
+    size_t bytes;
+    bool meets(const Span& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+        return at && o.at && bytes && o.bytes && a < b + o.bytes && b < a + bytes;
+    }
+    bool apart(std::initializer_list<Span> others) const {
+        return std::none_of(others.begin(), others.end(), [&](const Span& o) { return meets(o); });
+    }
+    bool apart_or_one_of(std::initializer_list<Span> others) const {
+        return std::none_of(others.begin(), others.end(), [&](const Span& o) { return meets(o) && (o.at != at || o.bytes != bytes); });
+    }
+};
+size_t type_bytes(int32_t type) { return type == MOE_F32 ? 4 : 2; }
+
 }  // namespace
 }  // namespace moe
 
@@ -642,8 +661,13 @@ extern "C" int moe_layer_norm_fwd(const void* x, const void* residual, const flo
     if (rows == 0) return MOE_OK;
     st = check_given({x, weight, y, rstd}, {residual, bias, total, mean});
     if (st != MOE_OK) return st;
-    // a row's total is stored before its y: one of them would be lost
-    if (y == total) return MOE_ERR_INVALID_ARG;
+    const size_t n = static_cast<size_t>(rows) * D, row = static_cast<size_t>(rows) * sizeof(float), col = static_cast<size_t>(D) * sizeof(float);
+    const Span sx{x, n * type_bytes(x_type)}, sr{residual, sx.bytes}, sw{weight, col}, sb{bias, col}, sh{total, sx.bytes},
+        sy{y, n * type_bytes(y_type)}, sm{mean, row}, ss{rstd, row};
+    // (a row's total is stored before its y: one of them would be lost)
+    if (!sh.apart_or_one_of({sx, sr}) || !sh.apart({sw, sb, sy, sm, ss}) || !sy.apart_or_one_of({sx, sr}) ||
+        !sy.apart({sw, sb, sm, ss}) || !sm.apart({sx, sr, sw, sb, ss}) || !ss.apart({sx, sr, sw, sb}))
+        return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.total = total; a.y = y;
     a.mean = mean; a.rstd = rstd; a.rows = rows; a.D = D; a.centre = mean != nullptr; a.align = row_align(D);
@@ -671,7 +695,14 @@ extern "C" int moe_layer_norm_bwd(const void* dy, const void* h, const float* we
               : check_given({dweight, workspace}, {dbias});
     if (st != MOE_OK) return st;
     const int G = bwd_groups(rows, D);
-    if (workspace_bytes < moe_layer_norm_bwd_workspace_bytes(rows, D)) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_layer_norm_bwd_workspace_bytes(rows, D);
+    if (workspace_bytes < need) return MOE_ERR_INVALID_ARG;
+    const size_t n = static_cast<size_t>(rows) * D, row = static_cast<size_t>(rows) * sizeof(float), col = static_cast<size_t>(D) * sizeof(float);
+    const Span sy{dy, n * type_bytes(y_type)}, sh{h, n * type_bytes(x_type)}, sw{weight, col}, sm{mean, row}, ss{rstd, row},
+        sd{dtotal, sh.bytes}, sx{dx, sh.bytes}, sdw{dweight, col}, sdb{dbias, col}, sp{workspace, need};
+    if (!sx.apart_or_one_of({sy, sh, sd}) || !sx.apart({sw, sm, ss, sdw, sdb, sp}) || !sdw.apart({sy, sh, sd, sw, sm, ss, sdb, sp}) ||
+        !sdb.apart({sy, sh, sd, sw, sm, ss, sp}) || !sp.apart({sy, sh, sd, sw, sm, ss}))
+        return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = h; a.dy = dy; a.dtotal = dtotal; a.weight = weight; a.dx = dx;
     a.dweight = dweight; a.dbias = dbias; a.accumulate = accumulate;
