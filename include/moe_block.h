@@ -47,15 +47,18 @@ size_t moe_ffn_decode_workspace_bytes(int64_t N, int32_t H, int32_t I, int32_t E
  *   logits      in  float32 [N, E]
  *   x           in  bf16 [N, H]
  *   w1          in  bf16 [E, 2I, H], w2 in bf16 [E, H, I]
- *   residual    in  bf16 [N, H], added to each token's sum; may be null, and
- *                   may be y
+ *   residual    in  bf16 [N, H], added to each token's sum; may be null
  *   n_live      in  int32 [1], device scalar clamped to [0, N]; may be null (N).
  *                   Tokens at or past it route nowhere (ids -1, probabilities
  *                   0) and their rows of y are left as they were
  *   topk_ids    out int32 [N, K], topk_probs out float32 [N, K]: bit for bit
  *                   moe_route_dropless's
  *   y           out bf16 [N, H] = bf16( sum_k act_k W2[e_k]^T + residual ),
- *                   act_k = bf16( silu(x Wg^T) * (x Wu^T) * prob_k )
+ *                   act_k = bf16( silu(x Wg^T) * (x Wu^T) * prob_k ); may be
+ *                   residual or x
+ *
+ * Outputs (the workspace's bytes among them) that share memory with another
+ * buffer in any other way are refused.
  *
  * Sums are float32 and rounded once; between the products only the activation
  * is rounded, as everywhere in the layer.  The same inputs give the same bits;

@@ -36,6 +36,7 @@
 #include <initializer_list>
 
 #include "gemm_common.h"
+#include "span.h"
 #include "topk.h"
 #include "../../include/moe_block.h"
 
@@ -776,6 +777,13 @@ extern "C" int moe_ffn_decode(const float* logits, const uint16_t* x, const uint
     for (const void* q : needed)
         if (!aligned16(q)) return MOE_ERR_MISALIGNED;
     if (!aligned16(residual) || (reinterpret_cast<uintptr_t>(n_live) & 3u)) return MOE_ERR_MISALIGNED;
+    const size_t routes = static_cast<size_t>(N) * K, matrix = static_cast<size_t>(E) * H * I * 2;
+    const Span sl{logits, static_cast<size_t>(N) * E * 4}, sx{x, static_cast<size_t>(N) * H * 2}, s1{w1, 2 * matrix}, s2{w2, matrix},
+        sr{residual, sx.bytes}, sn{n_live, 4}, si{topk_ids, routes * 4}, sp{topk_probs, routes * 4},
+        sw{workspace, moe_ffn_decode_workspace_bytes(N, H, I, E, K)}, sy{y, sx.bytes};
+    if (!sy.apart_or_one_of({sx, sr}) || !sy.apart({sl, s1, s2, sn, si, sp, sw}) || !si.apart({sl, sx, s1, s2, sr, sn, sp, sw}) ||
+        !sp.apart({sl, sx, s1, s2, sr, sn, sw}) || !sw.apart({sl, sx, s1, s2, sr, sn}))
+        return MOE_ERR_INVALID_ARG;
     const double mean = static_cast<double>(N) * K / E;
     DecodeArgs a{};
     a.logits = logits; a.a = x; a.w = w1; a.n_live = n_live; a.topk_ids = topk_ids; a.topk_probs = topk_probs;

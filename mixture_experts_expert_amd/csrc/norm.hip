@@ -25,6 +25,7 @@
 #include <initializer_list>
 
 #include "gemm_common.h"
+#include "span.h"
 #include "../../include/moe_block.h"
 
 namespace moe {
@@ -629,23 +630,6 @@ int check_given(std::initializer_list<const void*> needed, std::initializer_list
     return MOE_OK;
 }
 
-// A buffer of a call.  What is written may share memory with nothing else of the
-// call, or, row by row, be one of the buffers that are named: a row is stored while
-// others are still to be read.
-struct Span {
-    const void* at;
-    size_t bytes;
-    bool meets(const Span& o) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
-        return at && o.at && bytes && o.bytes && a < b + o.bytes && b < a + bytes;
-    }
-    bool apart(std::initializer_list<Span> others) const {
-        return std::none_of(others.begin(), others.end(), [&](const Span& o) { return meets(o); });
-    }
-    bool apart_or_one_of(std::initializer_list<Span> others) const {
-        return std::none_of(others.begin(), others.end(), [&](const Span& o) { return meets(o) && (o.at != at || o.bytes != bytes); });
-    }
-};
 size_t type_bytes(int32_t type) { return type == MOE_F32 ? 4 : 2; }
 
 }  // namespace
