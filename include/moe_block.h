@@ -196,7 +196,8 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, si
  *   grad_norm  in  float32 [1], device scalar (moe_grad_norm's); may be null.
  *                  Not finite: the call leaves everything as it was, step included
  *   max_norm   > 0, used with grad_norm only
- *   step       in/out int32 [1], device scalar: steps taken so far; becomes t
+ *   step       in/out int32 [1], device scalar: steps taken so far (clamped to
+ *                  [0, 2^31 - 2]); becomes t
  *
  * 0 <= beta < 1, eps >= 0. */
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,

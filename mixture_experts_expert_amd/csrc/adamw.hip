@@ -510,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
     }
     const float norm = b.grad_norm ? b.grad_norm[0] : 0.0f;
     const float lr = b.lr[0];
-    const int t = __builtin_amdgcn_readfirstlane(b.step[0]) + 1;
+    const int t = min(max(__builtin_amdgcn_readfirstlane(b.step[0]), 0), INT32_MAX - 1) + 1;
     // infinite or NaN: nothing is written, the step is not taken
     if ((__float_as_uint(norm) & 0x7F800000u) == 0x7F800000u) return;
     if (there) {

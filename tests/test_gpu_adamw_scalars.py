@@ -1,0 +1,37 @@
+"""AdamW's device scalars and eps at the ends of their ranges."""
+
+import pytest
+import torch
+
+from mixture_experts_expert_amd import MoEAdamW
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def optimizer(state, step, n=5000, g=0.5, **kw):
+    return MoEAdamW([torch.ones(n, device=DEV)], [torch.full((n,), g, device=DEV)], lr=1e-3, weight_decay=0.0, state=state,
+                    step=step, **kw)
+
+
+@pytest.mark.parametrize("state", ["f32", "q8"])
+@pytest.mark.parametrize("step", [-1, -7, -(1 << 31)])
+def test_a_step_number_below_0_counts_as_0(state, step):
+    a, b = optimizer(state, step), optimizer(state, 0)
+    for o in (a, b):
+        o.step_()
+    assert a.step.item() == 1 and torch.equal(a.params[0], b.params[0]) and torch.isfinite(a.params[0]).all()
+    assert all(torch.equal(x, y) for x, y in zip(sum(a.moments.values(), []), sum(b.moments.values(), [])))
+
+
+@pytest.mark.parametrize("state", ["f32", "q8"])
+def test_the_last_step_number_stays(state):
+    top = (1 << 31) - 1
+    for step in (top - 1, top):
+        o = optimizer(state, step)
+        o.step_()
+        assert o.step.item() == top
+        # the corrections have become 1: m 0.05, root sqrt(0.05 / 4), each within 8u and the rounding of p
+        want = 1 - 1e-3 * 0.05 / (0.0125 ** 0.5 + 1e-8)
+        assert (o.params[0].double() - want).abs().max() < 2.0 ** -22
