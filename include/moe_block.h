@@ -199,7 +199,8 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, si
  *   step       in/out int32 [1], device scalar: steps taken so far (clamped to
  *                  [0, 2^31 - 2]); becomes t
  *
- * 0 <= beta < 1, eps >= 0. */
+ * 0 <= beta < 1; eps 0 (an element that has had no gradient then becomes NaN, 0 / 0)
+ * or 2^-126 and more. */
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_t plan_bytes,
                    const float* lr, double beta1, double beta2, double eps, const float* grad_norm,
                    double max_norm, int32_t* step, hipStream_t stream);

@@ -742,6 +742,8 @@ int adamw_step(const moe_adamw_tensor* tensors, int32_t count, void* plan, size_
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !std::isfinite(eps) ||
         (grad_norm && !(max_norm > 0.0)))
         return MOE_ERR_INVALID_ARG;
+    // v_rcp_f32 takes a subnormal denominator for 0, which eps alone can be (a root is not: 2^-75 at least, or 0)
+    if (eps > 0.0 && static_cast<float>(eps) < 0x1p-126f) return MOE_ERR_UNSUPPORTED;
     if (!lr || !step || (random && s.entries > 0 && s.state != 8)) return MOE_ERR_INVALID_ARG;
     if (!aligned4(lr) || !aligned4(step) || !aligned4(grad_norm)) return MOE_ERR_MISALIGNED;
     AdamWArgs a;

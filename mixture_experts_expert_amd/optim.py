@@ -60,6 +60,8 @@ class MoEAdamW:
         b1, b2 = betas
         if not (0 <= b1 < 1 and 0 <= b2 < 1) or not eps >= 0:
             raise ValueError("need 0 <= beta < 1 and eps >= 0")
+        if 0 < eps < 2.0 ** -126:
+            raise ValueError("eps must be 0 or a normal float32 number, 2^-126 or more")
         if rounding not in (None, "stochastic", "nearest") or (rounding and state != "q8"):
             raise ValueError('rounding must be "stochastic" or "nearest", and goes with state "q8"')
         if not 0 <= seed < 1 << 32:

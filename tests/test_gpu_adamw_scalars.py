@@ -35,3 +35,17 @@ def test_the_last_step_number_stays(state):
         # the corrections have become 1: m 0.05, root sqrt(0.05 / 4), each within 8u and the rounding of p
         want = 1 - 1e-3 * 0.05 / (0.0125 ** 0.5 + 1e-8)
         assert (o.params[0].double() - want).abs().max() < 2.0 ** -22
+
+
+def test_the_smallest_eps():
+    """Nothing to divide by but eps: an element without a gradient stays, and 2^-126 is a divisor like any other."""
+    for eps in (2.0 ** -126, 2.0 ** -100):
+        o = MoEAdamW([torch.ones(64, device=DEV)], [torch.zeros(64, device=DEV)], lr=1e-3, weight_decay=0.0, eps=eps)
+        o.step_()
+        assert (o.params[0] == 1).all()
+        # v underflows to 0, m does not: p = 1 - 1e-3 * 2^-80 / eps, off by m's and the division's 8u
+        o.grads[0].fill_(2.0 ** -80)
+        o.step.zero_()
+        o.step_()
+        move = 1e-3 * 2.0 ** -80 / eps
+        assert ((o.params[0].double() - (1 - move)).abs() <= 2.0 ** -20 * (1 + move)).all()
