@@ -14,7 +14,8 @@
 // Measured: 75.5 M elements with bf16 parameters, float32 master copies and
 // gradients: norm 41 to 55 us (5.5 to 7.4 TB/s; behind a step that has just written
 // everything, its reads compete with the write-back), step 390 with moments in 32
-// bits (6.2 TB/s), 221 in 8 (6.2); 300 tensors of 2.9 M elements in all: 6.7 + 14.
+// bits (6.2 TB/s), in 8 222 rounded to nearest (6.2), 227 at random; 300 tensors of
+// 2.9 M elements in all: 6.7 + 14.
 #include <math.h>
 
 #include <algorithm>
@@ -480,8 +481,10 @@ struct AdamWScalars {
 enum State { kFloats, kNearest, kRandom };
 
 // A workgroup a chunk: all its loads are issued before the scalars are looked at.
+// With 8-bit moments six waves a SIMD (80 registers; at 81 five: 231 us instead of
+// 222 for 75 M elements).
 template <State STATE>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
+__global__ __launch_bounds__(kThreads, STATE == kFloats ? 1 : 6) void adamw_kernel(AdamWArgs b) {
     constexpr bool Q8 = STATE != kFloats;
     const int c = b.chunk0 + static_cast<int>(blockIdx.x);
     const bool there = c < b.chunks;                 // (without any element one workgroup moves the step alone)
@@ -537,11 +540,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs b) {
             s.update(g[i], m[i], v[i], root, p[i]);
             if (Q8) {
                 // elements past the end are zeros and take no part in the scale
-                const uint32_t am = group_max(m[i]), ar = group_max(root);
-                const int bm = STATE == kRandom ? first_scale_above(am) : first_scale(am);
-                const int br = STATE == kRandom ? root_scale_above(ar) : root_scale(ar);
-                store8(static_cast<uint8_t*>(e.m), at, n, STATE == kRandom ? first_codes_random(m[i], bm, key, at) : first_codes(m[i], bm));
-                store8(static_cast<uint8_t*>(e.v), at, n, STATE == kRandom ? root_codes_random(root, br, key, at) : root_codes(root, br));
+                int bm, br;
+                if constexpr (STATE == kRandom) {
+                    bm = first_scale_above(group_max(m[i]));
+                    br = root_scale_above(group_max(root));
+                    store8(static_cast<uint8_t*>(e.m), at, n, first_codes_random(m[i], bm, key, at));
+                    store8(static_cast<uint8_t*>(e.v), at, n, root_codes_random(root, br, key, at));
+                } else {
+                    bm = first_scale(group_max(m[i]));
+                    br = root_scale(group_max(root));
+                    store8(static_cast<uint8_t*>(e.m), at, n, first_codes(m[i], bm));
+                    store8(static_cast<uint8_t*>(e.v), at, n, root_codes(root, br));
+                }
                 if (at < n && at % kGroup == 0) {
                     e.m_scales[at / kGroup] = static_cast<uint8_t>(bm);
                     e.v_scales[at / kGroup] = static_cast<uint8_t>(br);
