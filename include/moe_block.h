@@ -42,7 +42,9 @@ int32_t moe_ffn_decode_max_tokens(void);
 size_t moe_ffn_decode_workspace_bytes(int64_t N, int32_t H, int32_t I, int32_t E, int32_t K);
 
 /* Steps 1-5 of the dropless form for 1 <= N <= 64 tokens (N == 0: no-op), in
- * two kernels that read each chosen expert's weights once:
+ * two kernels that read a chosen expert's weights once for every block of its
+ * routes: of up to 8, 16 or 32 in the first and 4, 8 or 16 in the second, by the
+ * routes an expert on average, so once where the batch is spread out:
  *
  *   logits      in  float32 [N, E]
  *   x           in  bf16 [N, H]
@@ -186,8 +188,8 @@ int moe_grad_norm(const moe_adamw_tensor* tensors, int32_t count, void* plan, si
  *   g = c * grad;  t = step + 1
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / ( sqrt(v) / sqrt(1 - beta2^t) + eps )
- * in float32, each result rounded once (8-bit moments: p moves by the moments
- * before they are rounded).
+ * in float32; roots and the division are the hardware's, good to 1 ulp (8-bit
+ * moments: p moves by the moments before they are rounded).
  * 8-bit moments are rounded to the nearest code, which loses moves of less than half
  * a code: right for a step or a few, but over a training run the moments do not
  * follow the gradients (moe_moments.h has figures, and the step for that).

@@ -110,7 +110,8 @@ class MoEBlockStep:
         b = self.block
         self.bwd.backward(d, self.u, b.w1, b.w2)
         self.d_router.addmm_(self.bwd.d_logits.t(), self.u.float())
-        # the experts' and the router's part are added in float32 and rounded once, to u's type
+        # the router's part is added in float32 to the experts' (bwd.dx, rounded to bf16 by the layer's backward), and
+        # their sum rounded to u's type
         du = torch.addmm(self.bwd.dx.float(), self.bwd.d_logits, b.router).to(torch.bfloat16)
         nat.moe_layer_norm_bwd(du, self.total, b.norm_weight, self.mean, self.rstd, self.dx, self.d_norm_weight,
                                self.d_norm_bias, self.workspace, dtotal=d, accumulate=True)

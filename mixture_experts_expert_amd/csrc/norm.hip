@@ -9,8 +9,10 @@
 // Both are HBM-bound passes: a row is read once, kept in registers as float32
 // through its sums, and written once.  TL lanes share a row, V pieces of 8
 // columns each, so a lane holds at most 32 columns, and the weights of its
-// columns stay in registers from row to row.  Every load and store is of 16
-// aligned bytes whatever D is, but for a row's first and last columns.
+// columns stay in registers from row to row.  Loads and stores are of 16 aligned
+// bytes whatever D is, but for a row's first and last columns; not aligned are those
+// of D 16377 to 16383, and, at widths above 1016 that are no multiple of 8, of a few
+// rows' backward by one workgroup after its first rows.
 //
 // TL and V are the fewest lanes, then pieces, that a row fits: idle ones take issue
 // slots (three pieces a lane instead of four where they do: bf16 rows of 8200
@@ -20,7 +22,7 @@
 // TB/s): forward with the addition 4.6 to 5.2 TB/s in bf16, 4.4 to 5.0 in float32,
 // backward with dtotal 4.0 to 5.0 and 4.1 to 5.3; rows of an odd number of bf16
 // 3.1 to 4.2 and 2.4 to 3.7, where the wave of a row's first and last columns takes
-// the time (1111 columns 112 us against 61 for 1112).  8 rows of 2048 take 3.8 us.
+// the time (1111 columns 110 us against 61 for 1112).  8 rows of 2048 take 3.8 us.
 #include <algorithm>
 #include <initializer_list>
 
@@ -129,8 +131,10 @@ struct Place {
     __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi; }
 };
 
-// The columns ahead of row r.  They are the same for every row a team works on,
-// since those are a multiple of 8 apart.
+// The columns ahead of row r, a team's first.  They are the same for every row it
+// works on where those are a multiple of 8 apart: everywhere but in a backward of
+// one workgroup of 1, 2 or 4 teams, whose later rows are loaded where this puts
+// them, off 16 bytes.
 __device__ __forceinline__ int columns_before(int64_t r, int D, int align) {
     return static_cast<int>(r & 7) * (D & 7) & align;
 }
@@ -548,7 +552,7 @@ int row_align(int D) { return D >= kPiece && pieces_on_16_bytes(D) <= kMaxNormDi
 int row_pieces(int D) { return row_align(D) ? pieces_on_16_bytes(D) : (D + kPiece - 1) / kPiece; }
 
 // Lanes a row and pieces a lane.  The backward's sums take twice the registers:
-// at most two pieces a lane.
+// two pieces a lane, four above 8192 columns, where they are in LDS.
 constexpr int bwd_lanes(int pieces) {
     return pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 128 ? 64 : pieces <= 256 ? 128
            : pieces <= 512 ? 256 : 512;

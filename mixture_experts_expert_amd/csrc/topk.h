@@ -1,7 +1,8 @@
-// Top-K of a token's router logits by a group of LPT lanes (internal): the
-// selection rounds and the softmax over the picks, shared by the routing calls
-// and the forward for a few tokens, whose picks and probabilities agree bit for
-// bit.
+// Top-K of a token's router logits by a group of LPT lanes (internal): the order
+// of logits, the selection rounds and the softmax over the picks.  The routing
+// calls use all of it; the forward for a few tokens shares the order, and the
+// rounds above 256 experts, and has rounds and a softmax of its own beside them,
+// of the same operations, so that picks and probabilities agree bit for bit.
 #pragma once
 
 #include <math.h>
