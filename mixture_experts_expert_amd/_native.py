@@ -1040,7 +1040,8 @@ def moe_layer_norm_bwd(dy, h, weight, mean, rstd, dx, dweight, dbias, workspace,
 class AdamWTable:
     """The tensors of moe_grad_norm and moe_adamw_step and their plan: per tensor its parameter,
     gradient, moments (codes with scale bytes: 8 bits), master copy and weight decay.  Holds the
-    tensors, so their memory stays theirs; the gradients are the buffers the backward writes.  The
+    memory that they have now, and goes on with it if a tensor is given other memory (`.data = `): a
+    table is made again then.  The gradients are the buffers the backward writes.  The
     plan is written on `stream` (None: the current one)."""
 
     def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, masters=None, weight_decay=0.0, stream=None):
@@ -1076,6 +1077,7 @@ class AdamWTable:
                 e.v_scales = _whole(sb, "a second moment's scales", -(-n // 32), u8, dev)
             if master is not None:
                 e.master = _whole(master, "a master copy", n, f32, dev)
+        self.memory = [t.untyped_storage() for ts in self.tensors for t in ts if t is not None]
         self.address = ctypes.addressof(self.array)
         self.bytes = int(lib.moe_adamw_plan_bytes(self.address, count))
         if self.bytes == 0:
