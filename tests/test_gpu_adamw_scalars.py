@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from mixture_experts_expert_amd import MoEAdamW
+from mixture_experts_expert_amd import MoEAdamW, moe_grad_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,24 @@ def test_the_smallest_eps():
         o.step_()
         move = 1e-3 * 2.0 ** -80 / eps
         assert ((o.params[0].double() - (1 - move)).abs() <= 2.0 ** -20 * (1 + move)).all()
+
+
+def test_the_norm_within_its_bound():
+    """Eight squares are added in float32, each addition and each product off by u of the sum so far: 8u of their sum at
+    most, 4u of its root, and the last rounding: 5u.  Groups of eight that a search found to round far to one side, all
+    alike so that nothing averages out, and random ones."""
+    u = 2.0 ** -24
+    g = torch.Generator().manual_seed(0)
+    x = (1 + torch.rand((1 << 16, 8), generator=g))
+    s = torch.zeros(1 << 16, dtype=torch.float64)
+    for j in range(8):                           # a fused product and addition, rounded to float32 (or both apart: as good)
+        s = (s + x[:, j].double().square()).float().double()
+    off = (s.sqrt() / x.double().square().sum(1).sqrt() - 1).abs()
+    assert off.max() > 1.5 * u
+    for row in off.topk(4).indices.tolist() + [0]:
+        for dt in (torch.float32, torch.bfloat16):
+            grad = x[row].repeat(1 << 12).to(dt).to(DEV)
+            opt = MoEAdamW([torch.zeros(grad.numel(), device=DEV)], [grad], max_norm=1.0)
+            moe_grad_norm(opt.table, opt.norm)
+            want = grad.double().square().sum().sqrt().item()
+            assert abs(opt.norm.item() - want) <= 5 * u * want
