@@ -18,7 +18,8 @@ Pages followed (cited by title and section):
 
 Parity status per function is listed in the module docstrings of
 ``oracle.moe`` (forward), ``oracle.backward`` (backward) and
-``oracle.lowbit`` (block-scaled storage).
+``oracle.lowbit`` (block-scaled storage); ``oracle.moments`` holds the
+roundings of an optimizer's 8-bit moments, which the pages do not have.
 """
 
 from .moe import (  # noqa: F401

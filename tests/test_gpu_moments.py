@@ -202,3 +202,18 @@ def test_how_moments_are_rounded_is_said():
             assert MoEAdamW([p], [g], state="q8", moments=fresh.moments, rounding=k).rounding == k
     with pytest.warns(UserWarning, match="do not follow"):
         assert MoEAdamW([p], [g], state="q8", moments=fresh.moments).rounding == "nearest"
+
+
+def test_a_run_that_goes_on():
+    """Another optimizer with the state, the step and the seed takes the same steps."""
+    a = make([5000, 33], 6, pt=BF16, masters="make", lr=1e-3, max_norm=0.02, seed=11)
+    for _ in range(2):
+        a.step_()
+    copy = {k: [t.clone() for t in v] for k, v in a.moments.items()}
+    b = MoEAdamW([p.clone() for p in a.params], a.grads, lr=1e-3, betas=(B1, B2), max_norm=0.02, state="q8", moments=copy,
+                 masters=[m.clone() for m in a.masters], step=a.step.clone(), rounding="stochastic", seed=11)
+    for _ in range(3):
+        a.step_(), b.step_()
+    assert a.step.item() == b.step.item() == 5
+    assert all(torch.equal(x, y) for x, y in zip(a.params + a.masters + sum(a.moments.values(), []),
+                                                 b.params + b.masters + sum(b.moments.values(), [])))
